@@ -20,6 +20,9 @@
  *   mfa_decode          attends a few query rows to selected 64-key blocks of a
  *                       long cache, split over CTAs (the selected-key flash
  *                       attention pull request).
+ *   mfa_tree_decode     attends a tree of drafted tokens to a cache;
+ *                       mfa_key_weights sums the weights its keys got, and
+ *                       mfa_evict_select / mfa_cache_compact evict by them.
  * mfa_fwd_bias adds an ALiBi bias to mfa_fwd, mfa_mask_from_sparse_mode turns
  * an Ascend sparse mode into a mask description, and mfa_fwd_noalloc runs the
  * map build and forward pass without any buffer from the caller but the tensors.
@@ -389,6 +392,120 @@ size_t mfa_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Nq
 mfa_status mfa_decode(const mfa_tensor* q, const mfa_tensor* k, const mfa_tensor* v, const int32_t* sel,
                       int32_t sel_k, const mfa_tensor* out, float* lse, int32_t n_split, void* workspace,
                       size_t workspace_bytes, uint32_t* dev_err, void* stream);
+
+/* ---- Drafted tokens over a cache, the keys' attention weights, eviction ----
+ *
+ * Three operators for serving from one contiguous cache, k and v [B, Hkv, N, D]
+ * bf16, of which batch b holds lens[b] keys (rows 0 .. lens[b] - 1). They are
+ * this library's own definitions; the pages have no counterpart.
+ *
+ * The rows. A call has T query rows per batch, the nodes of a tree of drafted
+ * tokens. Their keys and values are already in the cache, node t of batch b
+ * in row lens[b] + t. `parents` (DEVICE int32 [B, T]) gives each node's parent:
+ *   parents[b, t] in [0, t)   that node;
+ *   -1                        the node follows the sequence's last key;
+ *   -2                        no node: a padding row. It sees no key (out = 0,
+ *                             lse = -inf) and its key is seen by no row.
+ * Row t sees every key before lens[b], its own key and its ancestors' keys.
+ * parents == NULL is a chain, parents[b, t] = t - 1: causal attention of the
+ * last T tokens. T = 1 with parents == NULL is ordinary decoding.
+ * `lens` (DEVICE int32 [B]) is read on the device, so that a captured graph can
+ * be replayed as the sequences grow. Problems that only the device sees set
+ * MFA_DEVERR_BOUNDS in *dev_err: a length outside [0, N - T] (it is clamped to
+ * [0, N], and nodes whose row would lie at or past N are seen by nobody), a
+ * parent outside [-2, t), a parent that is itself a padding row (the way up
+ * ends there).
+ * Cache rows at or past lens[b] + T, padding nodes' rows and masked nodes' keys
+ * may hold anything, infinities and NaN included. A row that sees a DRAFTED
+ * key whose value row holds an infinity or a NaN gets NaN in all D columns. */
+
+/* Largest T with a tree (parents != NULL). */
+#define MFA_TREE_MAX_NODES 256
+
+/* Bytes of the DEVICE workspace mfa_tree_decode needs (0 on invalid sizes).
+ * It depends on the current device's SM count, not on the lengths. Host only. */
+size_t mfa_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t D);
+
+/* Attention of T drafted tokens per sequence over the cache, on `stream`:
+ * out = softmax(q k^T / sqrt(D)) v over the keys each row sees.
+ *   q, out  [B, Hq, T, D] bf16;  k, v [B, Hkv, N, D] bf16;  D in {64, 128, 256};
+ *           Hq % Hkv == 0 (any group size); stride[3] == 1, other strides
+ *           and base addresses 16-byte aligned. 1 <= N < 2^30.
+ *   lens, parents  as above; T <= MFA_TREE_MAX_NODES unless parents is NULL.
+ *   lse     float32 [B, Hq, T] contiguous, natural log.
+ *   workspace  DEVICE, 256-byte aligned, mfa_tree_decode_workspace_bytes bytes;
+ *           no contents are needed on entry. Calls that share one must not
+ *           overlap on the GPU.
+ *   dev_err DEVICE uint32 the kernels OR MFA_DEVERR_* bits into (required; the
+ *           caller clears it).
+ * B == 0 or T == 0 launches nothing. Errors: MFA_ERR_INVALID_ARG,
+ * MFA_ERR_SHAPE_MISMATCH, MFA_ERR_UNSUPPORTED (dtype, D, T, sizes, N == 0),
+ * MFA_ERR_CUDA. */
+mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, const mfa_tensor* v, const int32_t* lens,
+                           const int32_t* parents, const mfa_tensor* out, float* lse, void* workspace,
+                           size_t workspace_bytes, uint32_t* dev_err, void* stream);
+
+/* The attention weight every key got from a call's rows, on `stream`:
+ *   weights_out[b, g, j] = decay * weights_in[b, g, j]
+ *       + sum over heads h of group g and rows t that see key j of
+ *         row_scale[b, t] * exp(q[b, h, t] . k[b, g, j] / sqrt(D) - lse[b, h, t])
+ * for the keys j < lens[b] + T (padding nodes' keys get the decayed old value);
+ * other entries of weights_out are left as they were.
+ *   q [B, Hq, T, D], k [B, Hkv, N, D], lens, parents, lse: those of the
+ *       mfa_tree_decode call (or of any forward pass whose last T rows these are).
+ *   row_scale   DEVICE float32 [B, T], or NULL for ones. Rows of scale 0 (the
+ *       rejected drafts of a verified tree) are left out whatever they hold.
+ *   weights_in  DEVICE float32 [B, Hkv, N] contiguous, or NULL for zeros; may
+ *       be weights_out. Not read when decay is 0.
+ *   weights_out DEVICE float32 [B, Hkv, N] contiguous.
+ * Every key's sum is formed by one thread in a fixed order: the result does
+ * not change from run to run. T must be at least 1 (T == 0 is
+ * MFA_ERR_UNSUPPORTED); B == 0 launches nothing. Errors as mfa_tree_decode's. */
+mfa_status mfa_key_weights(const mfa_tensor* q, const mfa_tensor* k, const float* lse, const int32_t* lens,
+                           const int32_t* parents, const float* row_scale, const float* weights_in, float decay,
+                           float* weights_out, uint32_t* dev_err, void* stream);
+
+/* Choose the keys to keep, on `stream`. For every (b, g), with n = lens[b]
+ * clamped to [0, N]: all n keys when n <= budget; otherwise the last `recent`
+ * keys and, of the others, the budget - recent ones of the largest weight
+ * (ties go to the lowest index; -0 equals 0; NaN counts as -inf).
+ *   weights  DEVICE float32 [B, Hkv, N] contiguous.
+ *   keep     DEVICE int32 [B, Hkv, budget]: the kept keys' rows, ascending,
+ *            min(n, budget) of them, then -1.
+ *   new_lens DEVICE int32 [B]: min(n, budget). Must not be lens.
+ * 0 <= recent <= budget, budget >= 1. A length outside [0, N] sets
+ * MFA_DEVERR_BOUNDS. Errors: MFA_ERR_INVALID_ARG, MFA_ERR_UNSUPPORTED (N >= 2^30,
+ * B * Hkv > 2^24), MFA_ERR_CUDA. */
+mfa_status mfa_evict_select(const float* weights, const int32_t* lens, int32_t B, int32_t Hkv, int32_t N,
+                            int32_t budget, int32_t recent, int32_t* keep, int32_t* new_lens, uint32_t* dev_err,
+                            void* stream);
+
+/* Move cache rows together, on `stream`: for t < count[b] (clamped to
+ * [0, n_idx]), with s = start ? start[b] : 0,
+ *   row s + t of k_out, v_out and weights_out  <-  row s + idx[b, g, t] of k, v, weights.
+ * With mfa_evict_select's list this evicts the other keys; with start = lens
+ * and the accepted nodes of a tree, ascending, it commits a branch.
+ *   idx      DEVICE int32 [B, idx_heads, n_idx], idx_heads 1 (the same rows of
+ *            every head) or Hkv.
+ *   k, v     [B, Hkv, N, D]; k_out, v_out [B, Hkv, N_out, D]: bf16, D a multiple
+ *            of 8 up to 512, strides and addresses as for mfa_tree_decode.
+ *            Either the outputs are the inputs (same addresses and strides: in
+ *            place) or they share no byte with them.
+ *   weights [B, Hkv, N], weights_out [B, Hkv, N_out] DEVICE float32 contiguous, or
+ *            both NULL; in place exactly when k and v are.
+ *   zero_end DEVICE int32 [B] or NULL: weights_out[b, g, j] = 0 for
+ *            s + count[b] <= j < min(zero_end[b], N_out): the places that the
+ *            next keys will take.
+ * Rows not named above are left as they were. In place every entry must
+ * satisfy idx[t] >= t (an ascending list does); an entry that does not, or
+ * that names a row outside [0, N) or fills one outside [0, N_out), moves nothing
+ * and sets MFA_DEVERR_SEL. A row may be named more than once. Errors:
+ * MFA_ERR_INVALID_ARG (partly overlapping tensors among them),
+ * MFA_ERR_SHAPE_MISMATCH, MFA_ERR_UNSUPPORTED, MFA_ERR_CUDA. */
+mfa_status mfa_cache_compact(const mfa_tensor* k, const mfa_tensor* v, const float* weights, const int32_t* start,
+                             const int32_t* idx, int32_t idx_heads, int32_t n_idx, const int32_t* count,
+                             const int32_t* zero_end, const mfa_tensor* k_out, const mfa_tensor* v_out,
+                             float* weights_out, uint32_t* dev_err, void* stream);
 
 /* Synchronise `stream`, read the map's error word into *err_bits (if not
  * NULL) and return MFA_ERR_DEVICE when it is non-zero, MFA_OK otherwise. */

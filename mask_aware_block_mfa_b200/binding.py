@@ -7,6 +7,7 @@ missing or a call fails: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -25,9 +26,11 @@ DEVERR_BOUNDS, DEVERR_SEL, DEVERR_TIMEOUT, DEVERR_MAP = 1, 2, 4, 8
 EXPORTS = ("mfa_abi_version", "mfa_status_string", "mfa_tile_map_bytes", "mfa_tile_map_init",
            "mfa_build_tile_map", "mfa_fwd", "mfa_fwd_noalloc", "mfa_get_device_status",
            "mfa_mask_from_sparse_mode", "mfa_bwd_workspace_bytes", "mfa_bwd", "mfa_decode_workspace_bytes",
-           "mfa_decode", "mfa_fwd_bias", "mfa_test_arm_fwd_timeout")
+           "mfa_decode", "mfa_fwd_bias", "mfa_test_arm_fwd_timeout", "mfa_tree_decode_workspace_bytes",
+           "mfa_tree_decode", "mfa_key_weights", "mfa_evict_select", "mfa_cache_compact")
 BIAS_NONE, BIAS_ALIBI, BIAS_ALIBI_SQRT, BIAS_ALIBI_LEFT = 0, 1, 2, 3
 NOALLOC_SCRATCH_BYTES = 16 << 20
+TREE_MAX_NODES = 256
 
 
 class MfaTensor(ctypes.Structure):
@@ -121,6 +124,17 @@ def load(path: str = _LIB_PATH) -> ctypes.CDLL:
                                                                  ctypes.POINTER(MfaTensor), ctypes.c_void_p,
                                                                  ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
                                                                  ctypes.c_void_p, ctypes.c_void_p]
+    T, P, I = ctypes.POINTER(MfaTensor), ctypes.c_void_p, ctypes.c_int32
+    lib.mfa_tree_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.mfa_tree_decode_workspace_bytes.argtypes = [I] * 5
+    lib.mfa_tree_decode.restype = ctypes.c_int
+    lib.mfa_tree_decode.argtypes = [T, T, T, P, P, T, P, P, ctypes.c_size_t, P, P]
+    lib.mfa_key_weights.restype = ctypes.c_int
+    lib.mfa_key_weights.argtypes = [T, T, P, P, P, P, P, ctypes.c_float, P, P, P]
+    lib.mfa_evict_select.restype = ctypes.c_int
+    lib.mfa_evict_select.argtypes = [P, P, I, I, I, I, I, P, P, P, P]
+    lib.mfa_cache_compact.restype = ctypes.c_int
+    lib.mfa_cache_compact.argtypes = [T, T, P, P, P, I, I, P, P, T, T, P, P, P]
     lib.mfa_test_arm_fwd_timeout.restype = ctypes.c_int
     lib.mfa_test_arm_fwd_timeout.argtypes = [ctypes.c_uint32]
     if lib.mfa_abi_version() != 1:
@@ -426,6 +440,227 @@ class Decode:
         """Synchronise and return the device error bits (0 = none)."""
         torch.cuda.synchronize()
         return 0 if self.err is None else int(self.err.item())
+
+
+def _cache_desc(name: str, t, device, shape=None) -> MfaTensor:
+    """The C descriptor of a bf16 [B, H, N, D] tensor on `device` (the short way:
+    these calls take a few microseconds on the device)."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        _on_device(name, t, device)
+    if t.dtype is not torch.bfloat16 or t.dim() != 4:
+        raise ValueError(f"{name} must be a bfloat16 tensor of four dimensions, got {t.dtype} {tuple(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return MfaTensor(t.data_ptr(), MFA_BF16, 0, *t.shape, t.stride())
+
+
+def _array_ptr(name: str, t, device, dtype, shape) -> int:
+    """The address of a contiguous array handed over as a plain pointer."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype is not dtype or t.shape != shape or \
+            not t.is_contiguous():
+        _on_device(name, t, device, dtype, shape, contiguous=True)
+    return t.data_ptr()
+
+
+class _CacheOp:
+    """What the cache operators keep between calls: the device error word, made
+    here (outside any capture), so that the first call may already be captured."""
+
+    def __init__(self, device="cuda"):
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"the cache operators run on a CUDA device, got {device}")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device = device
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        home = torch.cuda.current_stream(device)
+        home.synchronize()  # calls may come on any stream
+        self._err = self.err.data_ptr()
+        self._kept = [(self.err, home.cuda_stream)]  # tensors of the object, and the stream whose memory they are
+
+    def status(self) -> int:
+        """Synchronise and return the device error bits since the last clear() (0 = none)."""
+        torch.cuda.synchronize(self.device)
+        return int(self.err.item())
+
+    def clear(self) -> None:
+        """Forget the error bits (on the current stream)."""
+        self.err.zero_()
+
+    @staticmethod
+    def _on_stream(stream):
+        """Memory allocated for a call belongs to the call's stream."""
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+    def _call(self, name: str, fn, *args, stream=None):
+        """Call an entry point on `stream` with the object's device current."""
+        if stream is not None:
+            _stream_ptr(stream, self.device)
+        else:
+            stream = torch.cuda.current_stream(self.device)
+        ptr = stream.cuda_stream
+        for t, home in self._kept:
+            if ptr != home:
+                t.record_stream(stream)
+        index = self.device.index
+        if torch.cuda.current_device() == index:
+            code = fn(*args, ptr)
+        else:
+            with torch.cuda.device(index):
+                code = fn(*args, ptr)
+        if code != MFA_OK:
+            _check(name, code)
+
+
+def tree_decode_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int) -> int:
+    return int(load().mfa_tree_decode_workspace_bytes(B, Hq, Hkv, T, D))
+
+
+class TreeDecode(_CacheOp):
+    """Attention of T drafted tokens per sequence, a tree or a chain, over a
+    cache (mfa_tree_decode): keeps the workspace between calls. Calls of one
+    object must not overlap on the GPU (one stream, or ordered streams)."""
+
+    def __init__(self, device="cuda"):
+        super().__init__(device)
+        self.ws = None
+        self._need = {}
+
+    def __call__(self, q, k, v, lens, parents=None, out=None, lse=None, stream=None):
+        """q [B, Hq, T, D], k / v [B, Hkv, N, D]: bf16; lens int32 [B]: keys held before the
+        drafted tokens, whose rows are lens[b] + t; parents int32 [B, T] (-1: the sequence's
+        end, -2: no node) or None for a chain. Returns out and the natural-log lse."""
+        dev = self.device
+        qd, kd = _cache_desc("q", q, dev), _cache_desc("k", k, dev)
+        vd = _cache_desc("v", v, dev, k.shape)
+        B_, Hq, T, D = q.shape
+        lens_p = _array_ptr("lens", lens, dev, torch.int32, (B_,))
+        par_p = None if parents is None else _array_ptr("parents", parents, dev, torch.int32, (B_, T))
+        key = (B_, Hq, k.shape[1], T, D)
+        need = self._need.get(key)
+        if need is None:
+            with _on(dev):
+                need = tree_decode_workspace_bytes(*key)
+            if need == 0:
+                raise ValueError("invalid tree decode sizes")
+            self._need[key] = need
+        if self.ws is None or self.ws.numel() < need or out is None or lse is None:
+            with self._on_stream(stream):
+                if self.ws is None or self.ws.numel() < need:
+                    # A smaller one stays: a graph captured with it may be replayed.
+                    self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
+                    self._kept.append((self.ws, torch.cuda.current_stream(dev).cuda_stream))
+                if out is None:
+                    out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+                if lse is None:
+                    lse = torch.empty(B_, Hq, T, dtype=torch.float32, device=dev)
+        od = _cache_desc("out", out, dev, q.shape)
+        lse_p = _array_ptr("lse", lse, dev, torch.float32, (B_, Hq, T))
+        self._call("mfa_tree_decode", load().mfa_tree_decode, qd, kd, vd, lens_p, par_p, od, lse_p, self.ws.data_ptr(),
+                   self.ws.numel(), self._err, stream=stream)
+        return out, lse
+
+
+class KeyWeights(_CacheOp):
+    """The attention weight every cached key got from a call's rows (mfa_key_weights)."""
+
+    def __call__(self, q, k, lse, lens, parents=None, row_scale=None, weights_in=None, decay=1.0, weights_out=None,
+                 stream=None):
+        """weights_out[b, g, j] = decay * weights_in[b, g, j] + the rows' softmax weights of key j,
+        summed over the group's heads and, times row_scale float32 [B, T], over the rows.
+        Weights are float32 [B, Hkv, N]; weights_in None is zeros, and may be weights_out
+        (None: new, zeros past the keys held). q, k, lens, parents, lse: TreeDecode's."""
+        dev = self.device
+        qd, kd = _cache_desc("q", q, dev), _cache_desc("k", k, dev)
+        B_, Hq, T, _ = q.shape
+        shape = k.shape[:3]
+        lens_p = _array_ptr("lens", lens, dev, torch.int32, (B_,))
+        par_p = None if parents is None else _array_ptr("parents", parents, dev, torch.int32, (B_, T))
+        lse_p = _array_ptr("lse", lse, dev, torch.float32, (B_, Hq, T))
+        row_p = None if row_scale is None else _array_ptr("row_scale", row_scale, dev, torch.float32, (B_, T))
+        in_p = None if weights_in is None else _array_ptr("weights_in", weights_in, dev, torch.float32, shape)
+        if weights_out is None:
+            with self._on_stream(stream):
+                weights_out = torch.zeros(shape, dtype=torch.float32, device=dev)
+        out_p = _array_ptr("weights_out", weights_out, dev, torch.float32, shape)
+        self._call("mfa_key_weights", load().mfa_key_weights, qd, kd, lse_p, lens_p, par_p, row_p, in_p, float(decay),
+                   out_p, self._err, stream=stream)
+        return weights_out
+
+
+class CacheCompact(_CacheOp):
+    """Moves cache rows together (mfa_cache_compact)."""
+
+    def __call__(self, k, v, idx, count, weights=None, start=None, zero_end=None, k_out=None, v_out=None,
+                 weights_out=None, stream=None):
+        """Row start[b] + t of k, v and weights takes row start[b] + idx[b, g, t], t < count[b]: in
+        place, or in k_out, v_out (and weights_out). idx int32 [B, Hkv or 1, n]; count, start and
+        zero_end int32 [B]. With start = lens and the accepted nodes, ascending, a branch of a
+        tree is committed; the caller then adds count to lens."""
+        dev = self.device
+        if (k_out is None) != (v_out is None):
+            raise ValueError("k_out and v_out are given together")
+        if k_out is not None and (weights is None) != (weights_out is None):
+            raise ValueError("weights and weights_out are given together")
+        kd, vd = _cache_desc("k", k, dev), _cache_desc("v", v, dev, k.shape)
+        B_, H, N, _ = k.shape
+        if k_out is None:
+            if weights_out is not None:
+                raise ValueError("weights_out without k_out and v_out")
+            kod, vod, weights_out, N_out = kd, vd, weights, N
+        else:
+            kod, vod = _cache_desc("k_out", k_out, dev), _cache_desc("v_out", v_out, dev, k_out.shape)
+            N_out = k_out.shape[2]
+        if idx.dim() != 3 or idx.shape[1] not in (1, H):
+            raise ValueError("idx must be an int32 [B, Hkv or 1, n] tensor")
+        idx_p = _array_ptr("idx", idx, dev, torch.int32, (B_, idx.shape[1], idx.shape[2]))
+        count_p = _array_ptr("count", count, dev, torch.int32, (B_,))
+        start_p = None if start is None else _array_ptr("start", start, dev, torch.int32, (B_,))
+        zero_p = None if zero_end is None else _array_ptr("zero_end", zero_end, dev, torch.int32, (B_,))
+        w_p = None if weights is None else _array_ptr("weights", weights, dev, torch.float32, (B_, H, N))
+        wo_p = None if weights is None else _array_ptr("weights_out", weights_out, dev, torch.float32, (B_, H, N_out))
+        self._call("mfa_cache_compact", load().mfa_cache_compact, kd, vd, w_p, start_p, idx_p, idx.shape[1],
+                   idx.shape[2], count_p, zero_p, kod, vod, wo_p, self._err, stream=stream)
+
+
+class Evictor(_CacheOp):
+    """Evicts a cache's keys by their accumulated attention weight: of every
+    (batch, head) the last `recent` keys stay and, up to `budget` in all, those
+    of the largest weight (mfa_evict_select, then mfa_cache_compact)."""
+
+    def __init__(self, budget: int, recent: int, device="cuda"):
+        super().__init__(device)
+        self.budget, self.recent = int(budget), int(recent)
+        self.compact = CacheCompact(device)
+        self.compact.err, self.compact._err, self.compact._kept = self.err, self._err, self._kept
+
+    def select(self, weights, lens, keep=None, new_lens=None, stream=None):
+        """keep int32 [B, Hkv, budget] (ascending rows, then -1) and new_lens int32 [B]."""
+        dev = self.device
+        if weights.dim() != 3:
+            raise ValueError("weights must be a float32 [B, Hkv, N] tensor")
+        B_, H, N = weights.shape
+        w_p = _array_ptr("weights", weights, dev, torch.float32, (B_, H, N))
+        lens_p = _array_ptr("lens", lens, dev, torch.int32, (B_,))
+        if keep is None or new_lens is None:
+            with self._on_stream(stream):
+                if keep is None:
+                    keep = torch.empty(B_, H, self.budget, dtype=torch.int32, device=dev)
+                if new_lens is None:
+                    new_lens = torch.empty(B_, dtype=torch.int32, device=dev)
+        keep_p = _array_ptr("keep", keep, dev, torch.int32, (B_, H, self.budget))
+        new_p = _array_ptr("new_lens", new_lens, dev, torch.int32, (B_,))
+        self._call("mfa_evict_select", load().mfa_evict_select, w_p, lens_p, B_, H, N, self.budget, self.recent,
+                   keep_p, new_p, self._err, stream=stream)
+        return keep, new_lens
+
+    def __call__(self, k, v, weights, lens, k_out=None, v_out=None, weights_out=None, zero_end=None, stream=None):
+        """Select, then move the kept rows of k, v and weights together, in place or into
+        k_out, v_out and weights_out. Returns keep and new_lens; lens is left to the caller."""
+        keep, new_lens = self.select(weights, lens, stream=stream)
+        self.compact(k, v, keep, new_lens, weights, None, zero_end, k_out, v_out, weights_out, stream=stream)
+        return keep, new_lens
 
 
 def arm_fwd_timeout_test(wait_us: int) -> None:
