@@ -36,6 +36,7 @@ namespace {
 constexpr int kKeys = 128;           // keys per tile
 constexpr int kChunk = kKeys * 128;  // bytes of 64 columns of a tile, 128-byte swizzled rows
 constexpr int kMaxRows = 128;        // query rows per row tile
+constexpr int kSeenWords = MFA_TREE_MAX_NODES / 32;
 constexpr float kLazy = 8.0f;        // a row's maximum moves when a score exceeds it by this (in powers of two)
 
 struct TreeParams {
@@ -52,124 +53,114 @@ struct TreeParams {
 
 // Tiles of a (batch, head) pair for row tile rt: up to the last node its rows can see.
 template <int NR>
-__device__ __forceinline__ int tiles_of(const TreeParams& p, int len, int rt) {
-  const int t_hi = min((rt * NR + NR - 1) / p.G, p.T - 1);
+__device__ __forceinline__ int last_node(const TreeParams& p, int rt) {
+  return min((rt * NR + NR - 1) / p.G, p.T - 1);
+}
+__device__ __forceinline__ int tiles_of(const TreeParams& p, int len, int t_hi) {
   return (min(len + t_hi + 1, p.N) + kKeys - 1) / kKeys;
 }
 
-// ---------------------------------------------------------------------------
-// Where a CTA's range begins. All of the block's threads call it: every thread
-// sums the tiles of a run of batches, a scan gives the total and finds the
-// batch that holds tile index `at(total)`.
-// ---------------------------------------------------------------------------
+// The pairs' tiles on the line of a row tile, for one warp: all lanes get the
+// line's length and the batch that holds tile `at(length)`, with the number of
+// tiles before that batch (b = -1: past the end). Every warp finds this for itself: for up to
+// 32 batches it is one load and two shuffle scans, without a block barrier.
 struct Start {
-  int64_t total, begin, before;  // tiles of the row tile's line; first of this CTA; first of batch b
-  int32_t b;
+  int total, begin, before, b;
 };
-
-template <int NR, int THREADS, typename At>
-__device__ __forceinline__ void find_start(const TreeParams& p, int rt, Start* s, int64_t* scan, At at) {
-  const int per = (p.B + THREADS - 1) / THREADS;
-  const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles_of<NR>(p, cache_len(p.lens, b, p.N), rt);
-  int64_t sum = mine;
+template <typename At>
+__device__ __forceinline__ Start find_start(const TreeParams& p, int t_hi, At at) {
+  const int lane = threadIdx.x & 31;
+  Start s{0, 0, 0, -1};
+  int keep = 0;  // tiles of batch `lane` (of the last 32)
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    keep = b0 + lane < p.B ? tiles_of(p, cache_len(p.lens, b0 + lane, p.N), t_hi) : 0;
+    s.total += __reduce_add_sync(0xffffffffu, keep);
+  }
+  s.total *= p.Hkv;
+  s.begin = at(s.total);
+  int done = 0;  // of the batches before
+  for (int b0 = 0; b0 < p.B && s.b < 0; b0 += 32) {
+    if (p.B > 32) keep = b0 + lane < p.B ? tiles_of(p, cache_len(p.lens, b0 + lane, p.N), t_hi) : 0;
+    int sum = keep;
 #pragma unroll
-  for (int w = 1; w < 32; w <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, sum, w);
-    if (lane >= w) sum += o;
-  }
-  if (lane == 31) scan[warp] = sum;
-  __syncthreads();
-  int64_t base = 0, total = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) base += scan[w];
-    total += scan[w];
-  }
-  total *= p.Hkv;
-  const int64_t begin = at(total);
-  int64_t first = (base + sum - mine) * p.Hkv;  // of batch b0
-  if (threadIdx.x == 0) {
-    s->total = total;
-    s->begin = begin;
-    s->b = -1;
-  }
-  __syncthreads();
-  if (begin >= first && begin < first + mine * p.Hkv) {
-    for (int b = b0; b < b1; ++b) {
-      const int64_t n = static_cast<int64_t>(tiles_of<NR>(p, cache_len(p.lens, b, p.N), rt)) * p.Hkv;
-      if (begin < first + n) {
-        s->before = first;
-        s->b = b;
-        break;
-      }
-      first += n;
+    for (int w = 1; w < 32; w <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, w);
+      if (lane >= w) sum += o;
     }
+    const unsigned in = __ballot_sync(0xffffffffu, s.begin < done + sum * p.Hkv);
+    if (in) {
+      const int l = __ffs(in) - 1;
+      s.b = b0 + l < p.B ? b0 + l : -1;
+      s.before = done + __shfl_sync(0xffffffffu, sum - keep, l) * p.Hkv;
+    }
+    done += __shfl_sync(0xffffffffu, sum, 31) * p.Hkv;
   }
-  __syncthreads();
+  return s;
 }
 
-__device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int groups) { return (total + groups - 1) / groups; }
+__device__ __forceinline__ int tiles_per_cta(int total, int groups) {
+  return static_cast<int>((static_cast<unsigned>(total) + groups - 1) / groups);
+}
 
 // The (batch, head) pairs of a CTA's range, one after the other.
-template <int NR>
 struct Walk {
   int b, g, t0, t1, len, nt;
-  int64_t left;  // tiles of the range not yet given out
-  __device__ __forceinline__ Walk(const TreeParams& p, int rt, const Start& s) {
-    const int64_t per = tiles_per_cta(s.total, p.groups);
-    left = min(per, s.total - s.begin);
+  int left;  // tiles of the range not yet given out
+  __device__ __forceinline__ Walk(const TreeParams& p, int t_hi, const Start& s, int count) {
+    left = count;
     b = s.b;
     len = cache_len(p.lens, b, p.N);
-    nt = tiles_of<NR>(p, len, rt);
-    const int64_t in = s.begin - s.before;
-    g = static_cast<int>(in / nt);
-    t0 = static_cast<int>(in % nt);
-    t1 = static_cast<int>(min(static_cast<int64_t>(nt), t0 + left));
+    nt = tiles_of(p, len, t_hi);
+    const int in = s.begin - s.before;
+    g = in / nt;
+    t0 = in - g * nt;
+    t1 = min(nt, t0 + left);
     left -= t1 - t0;
   }
   // The next pair; false at the range's end.
-  __device__ __forceinline__ bool next(const TreeParams& p, int rt) {
+  __device__ __forceinline__ bool next(const TreeParams& p, int t_hi) {
     if (left <= 0) return false;
     if (++g == p.Hkv) {
       g = 0;
       ++b;
       len = cache_len(p.lens, b, p.N);
-      nt = tiles_of<NR>(p, len, rt);
+      nt = tiles_of(p, len, t_hi);
     }
     t0 = 0;
-    t1 = static_cast<int>(min(static_cast<int64_t>(nt), left));
+    t1 = min(nt, left);
     left -= t1;
     return true;
   }
 };
 
 // ---------------------------------------------------------------------------
-// Layout. K and V come in units of 128 keys x 128 columns (64 for D = 64)
-// through one ring, a tile's K units before its V units. P's buffer is also
-// the scratch of everything rare (each softmax group its own 16 KB of it).
+// Layout. K and V come in units of 128 keys x 128 columns (64 for D = 64), each
+// through its own ring: a slot has one consumer (the S or the P.V warp), which
+// waits for its phases in order, so a parity always names the phase meant.
 // ---------------------------------------------------------------------------
 template <int D, int NR>
 struct Cfg {
-  static constexpr int kSoftWarps = NR == 128 ? 8 : 4;  // a group of 4 warps takes 64 rows
-  static constexpr int kGroups = kSoftWarps / 4;
-  static constexpr int kCols = NR / kGroups;            // rows (registers) per thread
-  static constexpr int kThreads = (kSoftWarps + 2) * 32;
+  static constexpr int kCols = NR < 32 ? NR : 32;       // rows (registers) per softmax thread
+  static constexpr int kGroups = NR / kCols;            // groups of 4 softmax warps
+  static constexpr int kSoftWarps = 4 * kGroups;
+  static constexpr int kThreads = (kSoftWarps + 3) * 32;
   static constexpr int kUnits = D == 256 ? 2 : 1;       // ring units of a K (or V) tile
   static constexpr int kUnit = (D == 64 ? 1 : 2) * kChunk;
-  static constexpr int kPBytes = kGroups * kChunk;
-  static constexpr int kPBufs = NR == 128 && D > 64 ? 1 : 2;
-  static constexpr int kRing = D == 64 ? 8 : (D == 256 && NR == 128 ? 4 : 5);
+  static constexpr int kPBytes = (NR + 63) / 64 * kChunk;
+  static constexpr int kPBufs = NR * D >= 128 * 128 ? 1 : 2;
+  static constexpr int kRingK = D == 64 ? 4 : 2;
+  static constexpr int kRingV = D == 64 ? 4 : (NR == 128 ? 2 : 3);
+  static constexpr int kRing = kRingK + kRingV;         // K's slots first
   static constexpr int kQ = 0;                          // NR rows x 128 B per 64 columns
   static constexpr int kQBytes = NR * D * 2;
   static constexpr int kRing0 = (kQBytes + 1023) / 1024 * 1024;
   static constexpr int kP = kRing0 + kRing * kUnit;     // behind the ring: D = 64 reads one chunk past its last unit
   static constexpr int kMisc = kP + kPBufs * kPBytes;
-  static constexpr int kMiscBytes = 2048;
+  static constexpr int kMiscBytes = NR * 14 + 16 * kCols * kGroups + 256;
   static constexpr int kBytes = kMisc + kMiscBytes + 1024;  // + slack for 1024-byte alignment
   static constexpr int kO = 2 * NR;                     // TMEM columns: S0 [0, NR) S1 [NR, 2 NR) O [2 NR, (2 + kUnits) NR)
   static constexpr int kTmem = 4 * NR;
+  static_assert(D != 256 || NR <= 64, "Q and P leave no room for the ring");
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(kTmem <= 512, "TMEM columns");
 };
@@ -244,33 +235,37 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     mfa_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ TreeParams p) {
   using C = Cfg<D, NR>;
-  constexpr int U = C::kUnits, RING = C::kRing, PB = C::kPBufs, W = C::kCols;
+  constexpr int U = C::kUnits, RK = C::kRingK, RV = C::kRingV, RING = C::kRing, PB = C::kPBufs, W = C::kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rt = blockIdx.x % p.rtiles, cta = blockIdx.x / p.rtiles;
 
   float* sNegM = reinterpret_cast<float*>(smem + C::kMisc);  // [NR] minus the row's maximum; 0 while it has none
-  float* sDelta = sNegM + NR;                                // [NR] how far it moved; at the end 1 / l
-  float* sAlpha = sDelta + NR;                               // [NR] 2^-delta
-  uint8_t* sSet = reinterpret_cast<uint8_t*>(sAlpha + NR);   // [NR] the row has a maximum
+  float* sDelta = sNegM + NR;                                // [NR] what the row's outputs are multiplied by
+  float* sAlpha = sDelta + NR;                               // [NR] what its sums are multiplied by as its maximum moves
+  float* sRed = sAlpha + NR;                                 // [groups][4][W] maxima, sums of the warps
+  uint8_t* sSet = reinterpret_cast<uint8_t*>(sRed + 4 * NR);  // [NR] the row has a maximum
   uint8_t* sPoison = sSet + NR;                              // [NR] the row sees a value that is not finite
   uint64_t* bars = reinterpret_cast<uint64_t*>(sPoison + NR);
   uint64_t* full = bars;               // [RING]
   uint64_t* empty = full + RING;       // [RING]
   uint64_t* q_full = empty + RING;     // Q of the next pair is in shared memory
   uint64_t* s_full = q_full + 1;       // [2]
-  uint64_t* s_empty = s_full + 2;      // [2] read into registers
+  uint64_t* s_empty = s_full + 2;      // [2] read for the last time
   uint64_t* p_full = s_empty + 2;      // [PB]
   uint64_t* p_empty = p_full + 2;      // [PB] P.V done
-  uint64_t* drain = p_empty + 2;
-  Start* sStart = reinterpret_cast<Start*>(drain + 1);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(sStart + 1);
+  uint64_t* drain = p_empty + 2;       // [2]
+  volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 2);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
-  static_assert(NR * 14 + (2 * RING + 10) * 8 + sizeof(Start) + 8 <= C::kMiscBytes, "misc");
+  static_assert((2 * RING + 11) * 8 + 8 <= 256, "misc");
 
   // The merging kernel may be scheduled now: it waits for this grid to end.
   asm volatile("griddepcontrol.launch_dependents;");
+  const int t_hi = last_node<NR>(p, rt);
+  const Start start = find_start(p, t_hi, [&](int total) { return cta * tiles_per_cta(total, p.groups); });
+  if (start.b < 0) return;  // more CTAs than tiles
+  const int total = min(tiles_per_cta(start.total, p.groups), start.total - start.begin);
   if (threadIdx.x == 0) {
     for (int i = 0; i < RING; ++i) {
       mbar_init(&full[i], 1);
@@ -281,16 +276,12 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       mbar_init(&s_empty[i], C::kSoftWarps * 32);
       mbar_init(&p_full[i], C::kSoftWarps * 32);
       mbar_init(&p_empty[i], 1);
+      mbar_init(&drain[i], 1);
     }
     mbar_init(q_full, C::kSoftWarps * 32);
-    mbar_init(drain, 1);
     *s_abort = 0;
     fence_mbarrier_init();
   }
-  find_start<NR, C::kThreads>(p, rt, sStart, reinterpret_cast<int64_t*>(smem + C::kP),
-                              [&](int64_t total) { return cta * tiles_per_cta(total, p.groups); });
-  const Start start = *sStart;
-  if (start.begin >= start.total) return;  // more CTAs than tiles
   if (warp == C::kSoftWarps) {
     tmem_alloc(s_tmem, C::kTmem);
     tmem_relinquish();
@@ -299,120 +290,100 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int total = static_cast<int>(min(tiles_per_cta(start.total, p.groups), start.total - start.begin));
+  Walk w(p, t_hi, start, total);
+  const uint32_t ring = smem_u32(smem + C::kRing0);
 
-  if (warp == C::kSoftWarps + 1) {
+  if (warp == C::kSoftWarps + 2) {
     // =================== TMA producer ===================
     if (lane == 0) {
-      Walk<NR> w(p, rt, start);
-      uint32_t idx = 0;  // units issued
+      uint32_t idx = 0;              // K (and V) units issued
+      uint32_t used = 0, phase = 0;  // slots: ever loaded, parity of the last load
       bool ok = true;
       do {
         for (int t = w.t0; t < w.t1 && ok; ++t) {
 #pragma unroll
-          for (int u = 0; u < 2 * U; ++u) {
-            const uint32_t slot = idx % RING;
-            if (idx >= RING && !(ok = mbar_wait(&empty[slot], (idx / RING - 1) & 1, s_abort))) break;
+          for (int x = 0; x < 2 * U; ++x) {
+            const bool isv = x >= U;
+            const uint32_t u = x % U, at = idx + u, ring_n = isv ? RV : RK;
+            const uint32_t slot = (isv ? RK : 0) + at % ring_n;
+            if (at >= ring_n && !(ok = mbar_wait(&empty[slot], (at / ring_n - 1) & 1, s_abort))) break;
             mbar_arrive_expect_tx(&full[slot], C::kUnit);
             uint8_t* dst = smem + C::kRing0 + slot * C::kUnit;
-            const CUtensorMap* map = u < U ? &tm_k : &tm_v;
 #pragma unroll
             for (int c = 0; c < C::kUnit / kChunk; ++c)
-              tma_load_4d(dst + c * kChunk, map, &full[slot], (u % U) * 128 + c * 64, t * kKeys, w.g, w.b);
-            ++idx;
+              tma_load_4d(dst + c * kChunk, isv ? &tm_v : &tm_k, &full[slot], u * 128 + c * 64, t * kKeys, w.g, w.b);
+            used |= 1u << slot;
+            phase = at / ring_n & 1 ? phase | 1u << slot : phase & ~(1u << slot);
           }
+          idx += U;
         }
-      } while (ok && w.next(p, rt));
+      } while (ok && w.next(p, t_hi));
       if (*s_abort) {
         // Loads in flight land before the CTA exits.
         volatile int no_abort = 0;
-        for (uint32_t j = idx > RING ? idx - RING : 0; j < idx; ++j) mbar_wait(&full[j % RING], (j / RING) & 1, &no_abort);
+        for (int i = 0; i < RING; ++i)
+          if (used >> i & 1) mbar_wait(&full[i], phase >> i & 1, &no_abort);
       }
     }
   } else if (warp == C::kSoftWarps) {
-    // =================== MMA issuer ===================
-    constexpr uint32_t idesc_s = idesc_tree(NR, false), idesc_o = idesc_tree(NR, true);
-    const uint32_t ring = smem_u32(smem + C::kRing0), q_addr = smem_u32(smem + C::kQ), p_addr = smem_u32(smem + C::kP);
-    Walk<NR> ws(p, rt, start), wp(p, rt, start);
-    int ts = ws.t0, tp = wp.t0;           // tiles of the next S and the next P.V
-    int ns = 0, np = 0, seg = 0;          // S and P.V issued; pairs begun
-    bool fresh_s = true, fresh_p = true;  // the next one is its pair's first
+    // =================== S^T = K Q^T ===================
+    constexpr uint32_t idesc = idesc_tree(NR, false);
+    const uint32_t q_addr = smem_u32(smem + C::kQ);
     bool ok = true;
-    uint64_t t_idle = 0;
-    auto have = [&](uint32_t first) {  // the U units from ring index `first` on have landed
-      bool x = true;
+    int n = 0, seg = 0;
+    do {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(q_full, seg & 1, s_abort));
+      for (int t = w.t0; t < w.t1 && ok; ++t, ++n) {
+        const uint32_t first = static_cast<uint32_t>(n) * U;
+        if (n >= 2 && !(ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[n & 1], ((n >> 1) - 1) & 1, s_abort)))) break;
 #pragma unroll
-      for (int u = 0; u < U; ++u) x &= mbar_test_wait(&full[(first + u) % RING], ((first + u) / RING) & 1);
-      return __all_sync(0xffffffffu, x) != 0;
-    };
-    // Whichever is ready first goes out: the next S, or the oldest pending P.V.
-    while (ok && np < total) {
-      bool did = false;
-      if (ns < total && ns <= np + 1) {
-        const uint32_t first = static_cast<uint32_t>(ns) * 2 * U;
-        if ((!fresh_s || __all_sync(0xffffffffu, mbar_test_wait(q_full, seg & 1))) &&
-            (ns < 2 || __all_sync(0xffffffffu, mbar_test_wait(&s_empty[ns & 1], ((ns >> 1) - 1) & 1))) && have(first)) {
+        for (int u = 0; u < U; ++u) {
+          const uint32_t slot = (first + u) % RK;
+          if (!(ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[slot], ((first + u) / RK) & 1, s_abort)))) break;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t slot = (first + (kk >> 3)) % RING;
-            const uint32_t ka = ring + slot * C::kUnit + ((kk >> 2) & (C::kUnit / kChunk - 1)) * kChunk + (kk & 3) * 32;
-            const uint32_t qb = q_addr + (kk >> 2) * (NR * 128) + (kk & 3) * 32;
-            umma_ss(tmem + (ns & 1) * NR, sdesc_sw128_lo(ka, 16), sdesc_sw128_lo(qb, 16), idesc_s, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / U / 16; ++kk) {
+            const uint32_t ka = ring + slot * C::kUnit + (kk >> 2) * kChunk + (kk & 3) * 32;
+            const uint32_t qb = q_addr + (u * 2 + (kk >> 2)) * (NR * 128) + (kk & 3) * 32;
+            umma_ss(tmem + (n & 1) * NR, sdesc_sw128_lo(ka, 16), sdesc_sw128_lo(qb, 16), idesc, u + kk > 0 ? 1u : 0u);
           }
-          umma_commit(&s_full[ns & 1]);
-#pragma unroll
-          for (int u = 0; u < U; ++u) umma_commit(&empty[(first + u) % RING]);
-          ++ns;
-          did = true;
-          fresh_s = false;
-          if (++ts == ws.t1 && ws.next(p, rt)) {
-            ts = ws.t0;
-            fresh_s = true;
-            ++seg;
-          }
+          umma_commit(&empty[slot]);
         }
+        umma_commit(&s_full[n & 1]);
       }
-      if (!did && np < ns) {
-        const uint32_t first = static_cast<uint32_t>(np) * 2 * U + U;
-        if (__all_sync(0xffffffffu, mbar_test_wait(&p_full[np % PB], (np / PB) & 1)) && have(first)) {
-          tc_fence_after();
-          const uint32_t pb = sdesc_sw128_lo(p_addr + (np % PB) * C::kPBytes, kChunk);
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const uint32_t va = sdesc_sw128_lo(ring + ((first + u) % RING) * C::kUnit, kChunk);
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_ss(tmem + C::kO + u * NR, va + kk * (16 * 128 / 16), pb + kk * (16 * 128 / 16), idesc_o,
-                      (!fresh_p || kk > 0) ? 1u : 0u);
-          }
-          umma_commit(&p_empty[np % PB]);
-#pragma unroll
-          for (int u = 0; u < U; ++u) umma_commit(&empty[(first + u) % RING]);
-          ++np;
-          did = true;
-          fresh_p = false;
-          if (++tp == wp.t1 && wp.next(p, rt)) {
-            tp = wp.t0;
-            fresh_p = true;
-          }
-        }
-      }
-      if (did) {
-        t_idle = 0;
-      } else {
-        // Bounded like every other wait.
-        if (*s_abort) ok = false;
-        const uint64_t now = global_timer_ns();
-        if (t_idle == 0) t_idle = now;
-        else if (now - t_idle > kWaitTimeoutNs) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-      }
-    }
-    if (!ok) *s_abort = 1;
-    umma_commit(drain);
+      ++seg;
+    } while (ok && w.next(p, t_hi));
+    umma_commit(&drain[0]);
     volatile int no_abort = 0;
-    mbar_wait(drain, 0, &no_abort);
+    mbar_wait(&drain[0], 0, &no_abort);
+  } else if (warp == C::kSoftWarps + 1) {
+    // =================== O^T += V^T P^T ===================
+    constexpr uint32_t idesc = idesc_tree(NR, true);
+    bool ok = true;
+    int n = 0;
+    do {
+      for (int t = w.t0; t < w.t1 && ok; ++t, ++n) {
+        const uint32_t first = static_cast<uint32_t>(n) * U;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_full[n % PB], (n / PB) & 1, s_abort)))) break;
+        const uint32_t pb = sdesc_sw128_lo(smem_u32(smem + C::kP) + (n % PB) * C::kPBytes, kChunk);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t slot = RK + (first + u) % RV;
+          if (!(ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[slot], ((first + u) / RV) & 1, s_abort)))) break;
+          tc_fence_after();
+          const uint32_t va = sdesc_sw128_lo(ring + slot * C::kUnit, kChunk);
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            umma_ss(tmem + C::kO + u * NR, va + kk * (16 * 128 / 16), pb + kk * (16 * 128 / 16), idesc,
+                    (t > w.t0 || kk > 0) ? 1u : 0u);
+          umma_commit(&empty[slot]);
+        }
+        umma_commit(&p_empty[n % PB]);
+      }
+    } while (ok && w.next(p, t_hi));
+    umma_commit(&drain[1]);
+    volatile int no_abort = 0;
+    mbar_wait(&drain[1], 0, &no_abort);
   } else {
     // =================== softmax and epilogue: a thread per key ===================
     // A failed wait raises *s_abort and the thread runs on (every later wait
@@ -420,30 +391,44 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     const int grp = warp >> 2, quad = warp & 3;
     const int tid = quad * 32 + lane;           // key of the tile; column of D
     const uint32_t bar = 1 + grp;               // the group's named barrier
+    constexpr uint32_t kAll = 1 + C::kGroups;   // all groups'
     const int col0 = grp * W;                   // its first row of the tile
     const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
     const int row0 = rt * NR + col0;            // its first row of the pair
     const int rows = min(W, p.R - row0);        // real ones (may be <= 0)
-    const float* negM = sNegM + col0;
+    float* negM = sNegM + col0;
     float* delta = sDelta + col0;
     float* alpha = sAlpha + col0;
-    Walk<NR> w(p, rt, start);
-    int n = 0;
-    do {
-      // ---- Q of the pair, zeros for rows that are none (every S of the previous pair is done) ----
-      const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
-      for (int i = threadIdx.x; i < NR * (D / 8); i += C::kSoftWarps * 32) {
-        const int r = i / (D / 8), u = i % (D / 8), row = rt * NR + r;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (row < p.R) {
-          const int t = row / p.G, h = w.g * p.G + row % p.G;
-          if (!par || __ldg(par + t) != -2)
-            x = __ldg(reinterpret_cast<const uint4*>(p.q + w.b * p.qs[0] + h * p.qs[1] + t * p.qs[2]) + u);
-        }
-        *reinterpret_cast<uint4*>(smem + C::kQ + (u >> 3) * (NR * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x;
+    float* red = sRed + 4 * col0;
+    // Q of a pair, zeros for rows that are none. (A padding row's Q may be
+    // anything: it reaches no other row.)
+    auto load_q = [&](int b, int g) {
+      constexpr int kPer = NR * (D / 8) / (C::kSoftWarps * 32), kStep = C::kSoftWarps * 32 / (D / 8);
+      const int u = threadIdx.x % (D / 8), r0 = threadIdx.x / (D / 8);
+      const __nv_bfloat16* src = p.q + b * p.qs[0] + static_cast<int64_t>(g) * p.G * p.qs[1] + u * 8;
+      uint4 x[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int row = rt * NR + r0 + k * kStep;
+        const int t = row / p.G, h = row - t * p.G;
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < p.R) x[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
       }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int r = r0 + k * kStep;
+        *reinterpret_cast<uint4*>(smem + C::kQ + (u >> 3) * (NR * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x[k];
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+    };
+    load_q(w.b, w.g);
+    int n = 0;
+    bool more;
+    do {
+      const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
       if (tid < W) {
-        sNegM[col0 + tid] = 0.f;
+        negM[tid] = 0.f;
         sSet[col0 + tid] = 0;
         sPoison[col0 + tid] = 0;
       }
@@ -453,8 +438,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
           if (e) atomicOr(p.err, e);
         }
       }
-      fence_proxy_async_smem();
-      mbar_arrive(q_full);
       named_barrier(bar, 128);
       uint64_t l[W / 2];
 #pragma unroll
@@ -462,150 +445,164 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 
       for (int t = w.t0; t < w.t1; ++t, ++n) {
         const int base = t * kKeys;
-        float x[W];
+        const uint32_t st = tm + (n & 1) * NR;  // the scores
+        uint8_t* pbuf = smem + C::kP + (n % PB) * C::kPBytes;
         mbar_wait(&s_full[n & 1], (n >> 1) & 1, s_abort);
         tc_fence_after();
-        tmem_ld_cols<W>(tm + (n & 1) * NR, x);
-        tc_fence_before();
-        mbar_arrive(&s_empty[n & 1]);
-        uint8_t* pbuf = smem + C::kP + (n % PB) * C::kPBytes + grp * kChunk;  // the group's 64 columns of P
-        const bool draft = base + kKeys > w.len;
-        if (draft) {
+        if (base + kKeys > w.len) {
           // ---- a tile with drafted keys, or the last: who sees what ----
-          mbar_wait(&p_empty[n % PB], ((n / PB) - 1) & 1, s_abort);  // pbuf is free (passes while it was never used)
+          // P's buffer is free (the wait passes while it was never used); its
+          // slice of the group holds the parents and the nodes each row sees.
+          mbar_wait(&p_empty[n % PB], ((n / PB) - 1) & 1, s_abort);
           const int j = base + tid, node = j - w.len;
           const bool held = j < min(w.len + p.T, p.N);
-          int* sPar = reinterpret_cast<int*>(pbuf);
-          uint32_t* sSeen = reinterpret_cast<uint32_t*>(pbuf + MFA_TREE_MAX_NODES * 4);  // [W][8]: the nodes a row sees
+          int* sPar = reinterpret_cast<int*>(pbuf + grp * (C::kPBytes / C::kGroups));
+          uint32_t* sSeen = reinterpret_cast<uint32_t*>(sPar + MFA_TREE_MAX_NODES);  // [W][kSeenWords]
           if (par) {
             for (int i = tid; i < p.T; i += 128) sPar[i] = __ldg(par + i);
+            for (int i = tid; i < W * kSeenWords; i += 128) sSeen[i] = 0u;
             named_barrier(bar, 128);
-            if (tid < W) {
-              uint32_t bits[MFA_TREE_MAX_NODES / 32] = {};
-              const int tt = tid < rows ? (row0 + tid) / p.G : 0;
-              if (tid < rows && sPar[tt] != -2)
-                for (int a = tt; a >= 0; a = tree_up(sPar, a)) {
-#pragma unroll
-                  for (int k = 0; k < MFA_TREE_MAX_NODES / 32; ++k) bits[k] |= (a >> 5) == k ? 1u << (a & 31) : 0u;
-                }
-#pragma unroll
-              for (int k = 0; k < MFA_TREE_MAX_NODES / 32; ++k) sSeen[tid * (MFA_TREE_MAX_NODES / 32) + k] = bits[k];
+            if (tid < rows && tid < W) {
+              const int tt = (row0 + tid) / p.G;
+              for (int a = sPar[tt] == -2 ? -1 : tt; a >= 0; a = tree_up(sPar, a))
+                sSeen[tid * kSeenWords + (a >> 5)] |= 1u << (a & 31);
             }
             named_barrier(bar, 128);
           }
           // V of a key that is not before the sequence's end must be finite,
-          // seen or not: 0 * inf would reach every row.
-          // (A test of a ring slot's phase needs its last occupant's to be over:
-          // it belongs to the tile before at the latest, whose P.V is awaited.)
+          // seen or not: 0 * inf would reach every row. (These threads have not
+          // followed the V ring's phases: with the last P.V done, every
+          // earlier phase of the slot is over.)
           if (n > 0) mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
+          uint4* vrow[U];
           bool finite = true;
           if (j >= w.len) {
-#pragma unroll 1
-            for (int u = 0; u < D / 8; ++u) {
-              const uint32_t unit = static_cast<uint32_t>(n) * 2 * U + U + (u >> 4);
-              if ((u & 15) == 0) mbar_wait(&full[unit % RING], (unit / RING) & 1, s_abort);
-              const uint4 y = *reinterpret_cast<const uint4*>(smem + C::kRing0 + (unit % RING) * C::kUnit + ((u >> 3) & 1) * kChunk +
-                                                              tid * 128 + (((u & 7) ^ (tid & 7)) << 4));
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t v = k == 0 ? y.x : k == 1 ? y.y : k == 2 ? y.z : y.w;
-                finite &= (v & 0x7f80u) != 0x7f80u && (v & 0x7f800000u) != 0x7f800000u;
-              }
+            for (int u = 0; u < U; ++u) {
+              const uint32_t unit = static_cast<uint32_t>(n) * U + u, slot = RK + unit % RV;
+              mbar_wait(&full[slot], (unit / RV) & 1, s_abort);
+              vrow[u] = reinterpret_cast<uint4*>(smem + C::kRing0 + slot * C::kUnit + tid * 128);
+            }
+            if (held) {
+              uint32_t bad = 0;
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll 8
+                for (int i = 0; i < D / U / 8; ++i) {
+                  const uint4 y = vrow[u][(i >> 3) * (kChunk / 16) + (i & 7)];
+                  bad |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u)) |
+                         (__vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u));
+                }
+              finite = bad == 0;
             }
           }
           int tt = row0 / p.G, hh = row0 % p.G;
-#pragma unroll
-          for (int c = 0; c < W; ++c) {
-            if (j >= w.len) {
-              bool see = held && c < rows;
-              if (see) see = par ? (sSeen[c * (MFA_TREE_MAX_NODES / 32) + (node >> 5)] >> (node & 31)) & 1 : node <= tt;
-              if (!see) x[c] = -INFINITY;
-              else if (!finite) sPoison[col0 + c] = 1;
-            }
-            if (++hh == p.G) {
-              hh = 0;
-              ++tt;
-            }
-          }
-          named_barrier(3, C::kSoftWarps * 32);  // both groups have looked
-          if (j >= w.len && !(held && finite) && grp == 0) {
 #pragma unroll 1
-            for (int u = 0; u < D / 8; ++u) {
-              const uint32_t unit = static_cast<uint32_t>(n) * 2 * U + U + (u >> 4);
-              *reinterpret_cast<uint4*>(smem + C::kRing0 + (unit % RING) * C::kUnit + ((u >> 3) & 1) * kChunk + tid * 128 +
-                                        (((u & 7) ^ (tid & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < W; c += 16) {
+            uint32_t x[16];
+            tmem_ld_32x32b_x16(st + c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (j >= w.len) {
+                bool see = held && c + i < rows;
+                if (see) see = par ? (sSeen[(c + i) * kSeenWords + (node >> 5)] >> (node & 31)) & 1 : node <= tt;
+                if (!see) x[i] = 0xff800000u;
+                else if (!finite) sPoison[col0 + c + i] = 1;
+              }
+              if (++hh == p.G) {
+                hh = 0;
+                ++tt;
+              }
             }
+            tmem_st_32x32b_x16(st + c, x);
+          }
+          tmem_st_wait();
+          named_barrier(kAll, C::kSoftWarps * 32);  // every group has looked
+          if (j >= w.len && !(held && finite) && grp == 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll 8
+              for (int i = 0; i < D / U / 8; ++i) vrow[u][(i >> 3) * (kChunk / 16) + (i & 7)] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         // ---- scores in powers of two, relative to the rows' maxima ----
-        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < W; c += 4) {
-          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(negM + c);
-          f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2, nm.x), x[c], x[c + 1]);
-          f2_unpack(f2_fma(f2_pack(x[c + 2], x[c + 3]), sc2, nm.y), x[c + 2], x[c + 3]);
-          mx[0] = fmax3(mx[0], x[c], x[c + 1]);
-          mx[1] = fmax3(mx[1], x[c + 2], x[c + 3]);
-        }
-        const bool first = t == w.t0;
-        if (vote_or(bar, fmaxf(mx[0], mx[1]) > kLazy) || first || draft) {
-          // ---- rare: new maxima ----
-          if (!draft) mbar_wait(&p_empty[n % PB], ((n / PB) - 1) & 1, s_abort);  // (passes while the buffer was never used)
-          float* sMax = reinterpret_cast<float*>(pbuf);  // [4][W]
-#pragma unroll
-          for (int c = 0; c < W; ++c) {
-            const float m = warp_max(x[c]);
-            if (lane == (c & 31)) sMax[quad * W + c] = m;
-          }
-          named_barrier(bar, 128);
-          bool moved = false;
-          if (tid < W) {
-            const float m = fmaxf(fmaxf(sMax[tid], sMax[W + tid]), fmaxf(sMax[2 * W + tid], sMax[3 * W + tid]));
-            const bool set = sSet[col0 + tid] != 0;
-            float d = 0.f;
-            if (m > (set ? kLazy : -INFINITY)) {
-              const float nm = sNegM[col0 + tid] - m;
-              d = sNegM[col0 + tid] - nm;
-              sNegM[col0 + tid] = nm;
-              sSet[col0 + tid] = 1;
-            }
-            delta[tid] = d;
-            alpha[tid] = set ? ex2_approx(-d) : 1.f;  // a row without a maximum has no sums yet
-            moved = set && d != 0.f;
-          }
-          moved = vote_or(bar, moved);
-#pragma unroll
-          for (int c = 0; c < W; c += 2) {
-            x[c] -= delta[c];
-            x[c + 1] -= delta[c + 1];
-          }
-          if (moved) {
-#pragma unroll
-            for (int c = 0; c < W / 2; ++c) {
-              float a, b;
-              f2_unpack(l[c], a, b);
-              l[c] = f2_pack(a * alpha[2 * c], b * alpha[2 * c + 1]);
-            }
-            // O holds every P.V of the pair before this tile's once the last is done.
-            mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
-            tc_fence_after();
+        // A pair's first tile sets them; a row may still have none in a tile
+        // of drafted keys only. Otherwise they move when a score exceeds one
+        // by more than kLazy.
+        float x[W];
+        bool renew = t == w.t0 || base >= w.len;
 #pragma unroll 1
-            for (int k = 0; k < U * (W / 16); ++k) {
-              const int c = (k % (W / 16)) * 16;
-              const uint32_t at = tm + C::kO + (k / (W / 16)) * NR + c;
-              uint32_t o[16];
-              tmem_ld_32x32b_x16(at, o);
+        for (bool again = false;; again = true) {
+          if (renew) {
+#pragma unroll 1
+            for (int c = 0; c < W; c += 16) {
+              uint32_t y[16];
+              tmem_ld_32x32b_x16(st + c, y);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[c + i]);
-              tmem_st_32x32b_x16(at, o);
+              for (int i = 0; i < 16; ++i) {
+                const float m = warp_max(fmaf(__uint_as_float(y[i]), p.scale_log2, negM[c + i]));
+                if (lane == i) red[quad * W + c + i] = m;
+              }
             }
-            tmem_st_wait();
-            tc_fence_before();
+            named_barrier(bar, 128);
+            bool moved = false;
+            if (tid < W) {
+              const float m = fmaxf(fmaxf(red[tid], red[W + tid]), fmaxf(red[2 * W + tid], red[3 * W + tid]));
+              const bool set = sSet[col0 + tid] != 0;
+              float d = 0.f;
+              if (m > (set ? kLazy : -INFINITY)) {
+                const float nm = negM[tid] - m;
+                d = negM[tid] - nm;
+                negM[tid] = nm;
+                sSet[col0 + tid] = 1;
+              }
+              alpha[tid] = set ? ex2_approx(-d) : 1.f;  // a row without a maximum has no sums yet
+              moved = set && d != 0.f;
+            }
+            if (vote_or(bar, moved)) {
+#pragma unroll
+              for (int c = 0; c < W / 2; ++c) {
+                float a, b;
+                f2_unpack(l[c], a, b);
+                l[c] = f2_pack(a * alpha[2 * c], b * alpha[2 * c + 1]);
+              }
+              // O holds every P.V of the pair before this tile's once the last is done.
+              mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
+              tc_fence_after();
+#pragma unroll 1
+              for (int k = 0; k < U * (W / 16); ++k) {
+                const int c = (k % (W / 16)) * 16;
+                const uint32_t at = tm + C::kO + (k / (W / 16)) * NR + c;
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(at, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[c + i]);
+                tmem_st_32x32b_x16(at, o);
+              }
+              tmem_st_wait();
+            }
           }
+          tmem_ld_cols<W>(st, x);
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < W; c += 4) {
+            const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(negM + c);
+            f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2, nm.x), x[c], x[c + 1]);
+            f2_unpack(f2_fma(f2_pack(x[c + 2], x[c + 3]), sc2, nm.y), x[c + 2], x[c + 3]);
+            mx[0] = fmax3(mx[0], x[c], x[c + 1]);
+            mx[1] = fmax3(mx[1], x[c + 2], x[c + 3]);
+          }
+          if (renew || again) break;
+          renew = vote_or(bar, fmaxf(mx[0], mx[1]) > kLazy);
+          if (!renew) break;
         }
-        // ---- weights: 2^x, their sums, and P in bf16 ----
+        tc_fence_before();
+        mbar_arrive(&s_empty[n & 1]);
+        // ---- weights 2^x, their sums, and P in bf16 ----
         uint32_t pk[W / 2];
 #pragma unroll
         for (int c = 0; c < W / 2; ++c) {
@@ -614,78 +611,85 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
           pk[c] = pack_bf16x2(e0, e1);
         }
         if (n >= PB) mbar_wait(&p_empty[n % PB], ((n / PB) - 1) & 1, s_abort);
+        uint8_t* prow = pbuf + (col0 >> 6) * kChunk + tid * 128;
 #pragma unroll
         for (int u = 0; u < W / 8; ++u)
-          *reinterpret_cast<uint4*>(pbuf + tid * 128 + ((u ^ (tid & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(prow + ((((col0 & 63) / 8 + u) ^ (tid & 7)) << 4)) =
               make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
         fence_proxy_async_smem();
         mbar_arrive(&p_full[n % PB]);
       }
 
+      // Q of the next pair now: every S of this one is done.
+      Walk nx = w;
+      more = nx.next(p, t_hi);
+      if (more) load_q(nx.b, nx.g);
+
       // ---- epilogue of the pair: its output, or this CTA's part of it ----
-      mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
-      tc_fence_after();
       const bool whole = w.t0 == 0 && w.t1 == w.nt;
       const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * NR + col0;
-      float* sL = reinterpret_cast<float*>(smem + C::kP + grp * kChunk);  // [4][W]
       {
         float v[W];
 #pragma unroll
         for (int c = 0; c < W / 2; ++c) f2_unpack(l[c], v[2 * c], v[2 * c + 1]);
         const int f = warp_sum_spread<W>(v, lane);
-        if (W == 64) {
-          sL[quad * W + f] = v[0];
-          sL[quad * W + f + 1] = v[1];
-        } else {
-          sL[quad * W + f] = v[0];  // (W = 16: two lanes write the same value)
-        }
+        red[quad * W + f] = v[0];  // (W = 16: two lanes write the same value)
       }
       named_barrier(bar, 128);
       if (tid < rows && tid < W) {
         const int tt = (row0 + tid) / p.G, h = w.g * p.G + (row0 + tid) % p.G;
         const bool dead = par && __ldg(par + tt) == -2;
-        const float sum = dead ? 0.f : (sL[tid] + sL[W + tid]) + (sL[2 * W + tid] + sL[3 * W + tid]);
-        const float m = -sNegM[col0 + tid];
-        // What the row's outputs are multiplied by; -1: it has none.
+        const float sum = dead ? 0.f : (red[tid] + red[W + tid]) + (red[2 * W + tid] + red[3 * W + tid]);
+        const float m = -negM[tid];
+        // -1: no output.
         delta[tid] = sum == 0.f ? -1.f : (sPoison[col0 + tid] ? NAN : (whole ? 1.f / sum : 1.f));
         if (whole) {
           p.lse[(static_cast<int64_t>(w.b) * p.Hq + h) * p.T + tt] =
               sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
         } else {
-          p.ml_part[(part + tid) * 2] = sum == 0.f ? -FLT_MAX : m;
-          p.ml_part[(part + tid) * 2 + 1] = sum;
+          *reinterpret_cast<float2*>(p.ml_part + (part + tid) * 2) = make_float2(sum == 0.f ? -FLT_MAX : m, sum);
         }
+        // Where the row goes, over what is no longer needed.
+        const int64_t to = w.b * p.os[0] + h * p.os[1] + tt * p.os[2];
+        reinterpret_cast<int*>(negM)[tid] = static_cast<int>(to);
+        reinterpret_cast<int*>(alpha)[tid] = static_cast<int>(to >> 32);
       }
       named_barrier(bar, 128);
+      mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
+      tc_fence_after();
 #pragma unroll 1
-      for (int u = 0; u < U; ++u) {
-        int tt = row0 / p.G, hh = row0 % p.G;
+      for (int k = 0; k < U * (W / 16); ++k) {
+        const int u = k / (W / 16), c0 = (k % (W / 16)) * 16;
         const int d = u * 128 + tid;
-#pragma unroll 1
-        for (int c = 0; c < rows && c < W; c += 16) {
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(tm + C::kO + u * NR + c, o);
-          tmem_ld_wait();
+        if (c0 >= rows) continue;
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(tm + C::kO + u * NR + c0, o);
+        tmem_ld_wait();
+        if (d < D) {
+          if (whole) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (c + i < rows && d < D) {
-              const float f = delta[c + i];
-              const float y = f == -1.f ? 0.f : __uint_as_float(o[i]) * f;
-              if (whole)
-                p.out[w.b * p.os[0] + static_cast<int64_t>(w.g * p.G + hh) * p.os[1] + tt * p.os[2] + d] = __float2bfloat16_rn(y);
-              else
-                p.o_part[(part + c + i) * D + d] = y;
+            for (int i = 0; i < 16; ++i) {
+              if (c0 + i >= rows) break;
+              const float f = delta[c0 + i];
+              const int64_t to = static_cast<int64_t>(static_cast<uint32_t>(reinterpret_cast<const int*>(negM)[c0 + i])) |
+                                 (static_cast<int64_t>(reinterpret_cast<const int*>(alpha)[c0 + i]) << 32);
+              p.out[to + d] = __float2bfloat16_rn(f == -1.f ? 0.f : __uint_as_float(o[i]) * f);
             }
-            if (++hh == p.G) {
-              hh = 0;
-              ++tt;
+          } else {
+            float* to = p.o_part + (part + c0) * D + d;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (c0 + i >= rows) break;
+              const float f = delta[c0 + i];
+              to[i * D] = f == -1.f ? 0.f : __uint_as_float(o[i]) * f;
             }
           }
         }
       }
       tc_fence_before();
-      named_barrier(bar, 128);  // delta and the scratch are read before the next pair writes them
-    } while (w.next(p, rt));
+      named_barrier(bar, 128);  // what the next pair overwrites has been read
+      w = nx;
+    } while (more);
     if (*s_abort && threadIdx.x == 0) atomicOr(p.err, MFA_DEVERR_TIMEOUT);
   }
   __syncthreads();
@@ -699,116 +703,98 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 // Merges the parts of every pair that was cut: with M = max m_s, out = sum o_s
 // 2^(m_s - M) / sum l_s 2^(m_s - M). A part without a visible key has
 // m = -FLT_MAX, l = 0, o = 0 (never -inf - -inf); all such: out = 0, lse = -inf.
-// A block takes `rpb` rows of a pair, 8 (few parts: a warp-sized group of
-// threads per row and its columns) or 1 (the groups split the parts).
+// A warp takes a row, a lane D / 32 of its columns and, for M and the
+// weights, every 32nd part: two rounds of loads. With few rows (SPLIT) a
+// block takes one row and its warps share the parts.
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = 8;
 
-template <int D, int NR>
-__global__ void __launch_bounds__(kMergeThreads) mfa_tree_merge(const __grid_constant__ TreeParams p, int rpb) {
-  constexpr int L = D / 4, S = kMergeThreads / L;  // threads per row, groups
-  __shared__ Start start;
-  __shared__ int64_t scan[kMergeThreads / 32];
-  __shared__ float4 so[S][L];
-  __shared__ float sl[S];
-  const int rt = blockIdx.y % p.rtiles, r0 = (blockIdx.y / p.rtiles) * rpb;  // rows of the row tile
+template <int D, int NR, bool SPLIT>
+__global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_constant__ TreeParams p) {
+  constexpr int E = D / 32, WS = SPLIT ? kMergeWarps : 1;
+  __shared__ float so[SPLIT ? kMergeWarps : 1][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rt = blockIdx.y % p.rtiles;
+  const int r = SPLIT ? blockIdx.y / p.rtiles : blockIdx.y / p.rtiles * kMergeWarps + warp;  // row of the row tile
   const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
-  const int rows = min(NR, p.R - rt * NR);
-  if (r0 >= rows) return;
+  if (r >= min(NR, p.R - rt * NR)) return;  // (SPLIT: the whole block)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // The pair's first tile on the row tile's line.
-  int64_t before = 0;
-  {
-    int64_t mine = 0, all = 0;
-    for (int x = threadIdx.x; x < p.B; x += kMergeThreads) {
-      const int n = tiles_of<NR>(p, cache_len(p.lens, x, p.N), rt);
-      all += n;
-      if (x < b) mine += n;
-    }
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
-      mine += __shfl_xor_sync(0xffffffffu, mine, w);
-      all += __shfl_xor_sync(0xffffffffu, all, w);
-    }
-    if ((threadIdx.x & 31) == 0) {
-      scan[threadIdx.x >> 5] = mine;
-      reinterpret_cast<int64_t*>(so)[threadIdx.x >> 5] = all;
-    }
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < kMergeThreads / 32; ++w) {
-      before += scan[w];
-      total += reinterpret_cast<int64_t*>(so)[w];
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) start.total = total * p.Hkv;
-    __syncthreads();
+  // The CTAs that met the pair.
+  const int t_hi = last_node<NR>(p, rt);
+  int before = 0, total = 0;
+  for (int x = lane; x < p.B; x += 32) {
+    const int n = tiles_of(p, cache_len(p.lens, x, p.N), t_hi);
+    total += n;
+    if (x < b) before += n;
   }
-  const int nt = tiles_of<NR>(p, cache_len(p.lens, b, p.N), rt);
-  const int64_t base = before * p.Hkv + static_cast<int64_t>(g) * nt;
-  const int64_t per = tiles_per_cta(start.total, p.groups);
-  const int64_t c0 = base / per, c1 = (base + nt - 1) / per;
+  total = __reduce_add_sync(0xffffffffu, total) * p.Hkv;
+  before = __reduce_add_sync(0xffffffffu, before);
+  const int nt = tiles_of(p, cache_len(p.lens, b, p.N), t_hi);
+  const int base = before * p.Hkv + g * nt, per = tiles_per_cta(total, p.groups);
+  const int c0 = base / per, c1 = (base + nt - 1) / per;
   if (c0 == c1) return;  // written by its only CTA
-  const int ns = static_cast<int>(c1 - c0 + 1);
-  // Row r's part s.
-  auto at = [&](int s, int r) {
+  const int ns = c1 - c0 + 1;
+  // Part s of the row: the first CTA met the pair's first tile (its second slot), the
+  // others begin inside it.
+  auto at = [&](int s) {
     const int64_t c = c0 + s;
-    return ((c * p.rtiles + rt) * 2 + (c * per > base ? 0 : 1)) * NR + r;
+    return ((c * p.rtiles + rt) * 2 + (s > 0 ? 0 : 1)) * NR + r;
   };
-  const int grp = threadIdx.x / L, d = (threadIdx.x % L) * 4;
-  auto write = [&](int r, float4 o, float l, float M) {
-    const int row = rt * NR + r, t = row / p.G, h = g * p.G + row % p.G;
-    const bool has = l != 0.f;
-    const float inv = has ? 1.f / l : 0.f;
-    uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (!has) w = make_uint2(0u, 0u);
-    *reinterpret_cast<uint2*>(p.out + b * p.os[0] + h * p.os[1] + t * p.os[2] + d) = w;
-    if (d == 0)
-      p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + t] = has ? (M + log2f(l)) * 0.69314718055994530942f : -INFINITY;
-  };
-  if (rpb > 1) {
-    for (int r = r0 + grp; r < min(r0 + rpb, rows); r += S) {
-      float M = -FLT_MAX, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < ns; ++s) M = fmaxf(M, p.ml_part[at(s, r) * 2]);
-#pragma unroll 4
-      for (int s = 0; s < ns; ++s) {
-        const int64_t x = at(s, r);
-        const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + x * 2);
-        const float4 y = *reinterpret_cast<const float4*>(p.o_part + x * D + d);
-        const float f = ex2_approx(ml.x - M);
-        l = fmaf(f, ml.y, l);
-        o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y); o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
-      }
-      write(r, o, l, M);
-    }
-    return;
-  }
-  float M = -FLT_MAX, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < ns; ++s) M = fmaxf(M, p.ml_part[at(s, r0) * 2]);
-#pragma unroll 4
-  for (int s = grp; s < ns; s += S) {
-    const int64_t x = at(s, r0);
-    const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + x * 2);
-    const float4 y = *reinterpret_cast<const float4*>(p.o_part + x * D + d);
-    const float f = ex2_approx(ml.x - M);
-    l = fmaf(f, ml.y, l);
-    o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y); o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
-  }
-  so[grp][d / 4] = o;
-  if (d == 0) sl[grp] = l;
-  __syncthreads();
-  if (grp == 0) {
+  float M = -FLT_MAX;
+  for (int s = lane; s < ns; s += 32) M = fmaxf(M, p.ml_part[at(s) * 2]);
+  M = warp_max(M);
+  float l = 0.f, o[E];
 #pragma unroll
-    for (int s = 1; s < S; ++s) {
-      const float4 y = so[s][d / 4];
-      o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
-      l += sl[s];
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int s0 = 0; s0 < ns; s0 += 32) {
+    float f = 0.f;
+    if (s0 + lane < ns) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + at(s0 + lane) * 2);
+      f = ex2_approx(ml.x - M);
+      l = fmaf(f, ml.y, l);
     }
-    write(r0, o, l, M);
+    const int hi = min(32, ns - s0);
+#pragma unroll 8
+    for (int s = SPLIT ? warp : 0; s < hi; s += WS) {
+      const float fs = __shfl_sync(0xffffffffu, f, s);
+      const float* y = p.o_part + at(s0 + s) * D + lane * E;
+      if constexpr (E == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(y);
+        o[0] = fmaf(fs, v.x, o[0]); o[1] = fmaf(fs, v.y, o[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(y + e);
+          o[e] = fmaf(fs, v.x, o[e]); o[e + 1] = fmaf(fs, v.y, o[e + 1]);
+          o[e + 2] = fmaf(fs, v.z, o[e + 2]); o[e + 3] = fmaf(fs, v.w, o[e + 3]);
+        }
+      }
+    }
   }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int x = 1; x < kMergeWarps; ++x) o[e] += so[x][lane * E + e];
+  }
+  const int row = rt * NR + r, t = row / p.G, h = g * p.G + row % p.G;
+  const bool has = l != 0.f;
+  const float inv = has ? 1.f / l : 0.f;
+  uint32_t* to = reinterpret_cast<uint32_t*>(p.out + b * p.os[0] + h * p.os[1] + t * p.os[2] + lane * E);
+  uint32_t y[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) y[e] = has ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+  if constexpr (E == 2) *to = y[0];
+  else if constexpr (E == 4) *reinterpret_cast<uint2*>(to) = make_uint2(y[0], y[1]);
+  else *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+  if (lane == 0)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + t] = has ? (M + log2f(l)) * 0.69314718055994530942f : -INFINITY;
 }
 
 // ---- host ----
@@ -817,15 +803,15 @@ struct TreePlan {
   int nr, rtiles, groups;
 };
 
-// Rows per tile: the smallest of 16, 32, 64, 128 that holds the R rows, or 128 and several
-// tiles. CTAs: one per SM, the row tiles side by side on the same keys; with
+// Rows per tile: the smallest of 16, 32, 64, 128 (D = 256: 64) that holds the R rows, or the
+// largest and several tiles. CTAs: one per SM, the row tiles side by side on the same keys; with
 // more than 8 row tiles about two per SM instead, so that an uneven number of
 // tiles costs less than the half-empty last wave.
-TreePlan plan_tree(int64_t R) {
+TreePlan plan_tree(int64_t R, int64_t D) {
   const int n_sm = device_sm_count();
   const int64_t sms = n_sm > 0 ? n_sm : 148;
   TreePlan pl;
-  pl.nr = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : kMaxRows;
+  pl.nr = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 || D == 256 ? 64 : kMaxRows;
   pl.rtiles = static_cast<int>(cdiv64(R, pl.nr));
   pl.groups = static_cast<int>(pl.rtiles <= 8 ? sms / pl.rtiles : cdiv64(2 * sms, pl.rtiles));
   if (pl.groups < 1) pl.groups = 1;
@@ -862,17 +848,19 @@ mfa_status launch_tree(const CUtensorMap& mk, const CUtensorMap& mv, const TreeP
   if (p.groups > 1) {
     const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
     const int rows = p.R < NR ? p.R : NR;
-    const int rpb = pairs * p.R <= 1024 ? 1 : 8;
+    const bool split = pairs * p.R <= 1024;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>((rows + rpb - 1) / rpb * p.rtiles));
-    cfg.blockDim = dim3(kMergeThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>((split ? rows : cdiv64(rows, kMergeWarps)) * p.rtiles));
+    cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, mfa_tree_merge<D, NR>, p, rpb) != cudaSuccess) return MFA_ERR_CUDA;
+    if ((split ? cudaLaunchKernelEx(&cfg, mfa_tree_merge<D, NR, true>, p)
+               : cudaLaunchKernelEx(&cfg, mfa_tree_merge<D, NR, false>, p)) != cudaSuccess)
+      return MFA_ERR_CUDA;
   }
   return MFA_OK;
 }
@@ -883,7 +871,9 @@ mfa_status launch_tree_rows(int nr, const CUtensorMap& mk, const CUtensorMap& mv
     case 16: return launch_tree<D, 16>(mk, mv, p, s);
     case 32: return launch_tree<D, 32>(mk, mv, p, s);
     case 64: return launch_tree<D, 64>(mk, mv, p, s);
-    default: return launch_tree<D, 128>(mk, mv, p, s);
+    default:
+      if constexpr (D == 256) return MFA_ERR_UNSUPPORTED;  // plan_tree gives no such tile
+      else return launch_tree<D, 128>(mk, mv, p, s);
   }
 }
 
@@ -895,7 +885,7 @@ extern "C" size_t mfa_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t
   if (B < 0 || Hq <= 0 || Hkv <= 0 || T < 0 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
   if (B == 0 || T == 0) return 256;
   size_t o_bytes;
-  return part_bytes(plan_tree(static_cast<int64_t>(T) * (Hq / Hkv)), D, &o_bytes);
+  return part_bytes(plan_tree(static_cast<int64_t>(T) * (Hq / Hkv), D), D, &o_bytes);
 }
 
 extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, const mfa_tensor* v,
@@ -911,8 +901,9 @@ extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, 
   if (v->B != k->B || v->H != k->H || v->N != k->N || v->D != k->D) return MFA_ERR_SHAPE_MISMATCH;
   if (out->B != q->B || out->H != q->H || out->N != q->N || out->D != q->D) return MFA_ERR_SHAPE_MISMATCH;
   if (empty) return MFA_OK;
+  if (k->B * k->H * cdiv64(k->N, kKeys) >= (int64_t(1) << 31)) return MFA_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
   const int64_t R = q->N * (q->H / k->H);
-  const TreePlan pl = plan_tree(R);
+  const TreePlan pl = plan_tree(R, q->D);
   size_t o_bytes;
   const size_t need = part_bytes(pl, q->D, &o_bytes);
   if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)

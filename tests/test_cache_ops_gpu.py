@@ -15,7 +15,7 @@ from mask_aware_block_mfa_b200 import binding as B
 from oracle import evict as OE
 from oracle import tree as OT
 
-from .cache_util import check_attention, make, random_trees, to_gpu, weights_tolerance
+from .cache_util import HALF_BF16, ULP, check_attention, make, random_trees, to_gpu, weights_tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -57,6 +57,56 @@ def test_tree_decode_matches_the_oracle(case):
     out, lse, err = decode(q, k, v, lens, parents)
     assert err == 0
     check_attention(out, lse, q, k, v, lens, parents)
+
+
+@pytest.mark.parametrize("D,G,T,tree", [(64, 2, 2, None), (64, 3, 10, "random"), (64, 4, 13, "random"), (64, 4, 32, "random"), (128, 2, 1, None),
+                                        (128, 4, 7, "random"), (128, 5, 10, "random"), (128, 4, 30, "random"), (256, 2, 3, None),
+                                        (256, 4, 8, "random"), (256, 6, 10, "random"), (256, 4, 30, "random")])
+def test_tree_decode_with_many_tiles_and_pairs_per_block(D, G, T, tree):
+    """Over 1500 tiles of 128 keys, so that every block walks ten or more, most of
+    them long pairs and some of them many short ones."""
+    lens = [9000, 40, 0, 5117, 300, 9728 - T, 128]
+    q, k, v, lens, parents = make(D + T, len(lens), 8 * G, 8, T, 9728, D, lens, tree, True)
+    op = B.TreeDecode()
+    args = [to_gpu(x) for x in (q, k, v, lens, parents)]
+    runs = [op(*args) for _ in range(3)]
+    assert op.status() == 0
+    for out, lse in runs[1:]:
+        assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
+    out, lse = (x.cpu() for x in runs[0])
+    ref_out, ref_lse = reference(args, D)
+    mass, _ = reference(args[:2] + [args[2].abs()] + args[3:], D)
+    tol_out, tol_lse = large_tolerance(args, mass, ref_out, ref_lse)
+    assert ((out.cuda().double() - ref_out).abs() <= tol_out).all()
+    empty = torch.isneginf(ref_lse)
+    assert torch.equal(torch.isneginf(lse.cuda()), empty)
+    assert ((lse.cuda().double() - ref_lse).abs() <= tol_lse)[~empty].all()
+
+
+def reference(args, D):
+    """The definition in 64 bits on the GPU, one batch at a time (large cases)."""
+    q, k, v, lens, parents = args
+    Bz, Hq, T, _ = q.shape
+    out = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    lse = torch.full((Bz, Hq, T), -math.inf, dtype=torch.float64, device="cuda")
+    for b in range(Bz):
+        end = int(lens[b]) + T
+        vis = torch.from_numpy(OT.visible(int(lens[b]), None if parents is None else parents[b].tolist(), T, k.shape[2])[:, :end]).cuda()
+        G = Hq // k.shape[1]
+        kk, vv = (x[b, :, :end].double().repeat_interleave(G, 0) for x in (k, v))
+        s = (q[b].double() @ kk.transpose(1, 2) / math.sqrt(D)).masked_fill(~vis, -math.inf)
+        lse[b] = s.logsumexp(-1)
+        out[b] = torch.where(vis.any(-1)[None, :, None], torch.nan_to_num((s - lse[b][..., None]).exp()) @ vv, 0.0)
+    return out, lse
+
+
+def large_tolerance(args, mass, out, lse):
+    """attention_tolerance with |q . k| bounded by |q| |k|, on the GPU; mass: sum of p |v|."""
+    q, k, _, lens, _ = args
+    n, D = int(lens.max()) + q.shape[2], q.shape[3]
+    ds = float((D + 4) * ULP * q.double().norm(dim=-1).max() * k.double().norm(dim=-1).max() / math.sqrt(D))
+    rel = 2 * ds + (n + 8) * ULP
+    return mass * (HALF_BF16 + rel) * (1 + HALF_BF16) + HALF_BF16 * out.abs() + 1e-30, ds + (n + 8) * ULP + 4 * ULP * lse.abs()
 
 
 @pytest.mark.parametrize("T,G", [(1, 4), (8, 4), (60, 2)])
