@@ -60,27 +60,28 @@ __device__ __forceinline__ int tiles_of(const TreeParams& p, int len, int t_hi) 
   return (min(len + t_hi + 1, p.N) + kKeys - 1) / kKeys;
 }
 
-// The pairs' tiles on the line of a row tile, for one warp: all lanes get the
-// line's length and the batch that holds tile `at(length)`, with the number of
-// tiles before that batch (b = -1: past the end). Every warp finds this for itself: for up to
+// The line that is cut: a pair counts its tiles and `extra` more before them, for
+// what it costs to begin and end one (Q, the first maxima, the epilogue).
+// For one warp: all lanes get the line's length and the batch that holds
+// place `at(length)`, with the length before that batch (b = -1: past the end). Every warp finds this for itself: for up to
 // 32 batches it is one load and two shuffle scans, without a block barrier.
 struct Start {
   int total, begin, before, b;
 };
 template <typename At>
-__device__ __forceinline__ Start find_start(const TreeParams& p, int t_hi, At at) {
+__device__ __forceinline__ Start find_start(const TreeParams& p, int t_hi, int extra, At at) {
   const int lane = threadIdx.x & 31;
   Start s{0, 0, 0, -1};
-  int keep = 0;  // tiles of batch `lane` (of the last 32)
+  int keep = 0;  // of batch `lane` of the last 32
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    keep = b0 + lane < p.B ? tiles_of(p, cache_len(p.lens, b0 + lane, p.N), t_hi) : 0;
+    keep = b0 + lane < p.B ? tiles_of(p, cache_len(p.lens, b0 + lane, p.N), t_hi) + extra : 0;
     s.total += __reduce_add_sync(0xffffffffu, keep);
   }
   s.total *= p.Hkv;
   s.begin = at(s.total);
   int done = 0;  // of the batches before
   for (int b0 = 0; b0 < p.B && s.b < 0; b0 += 32) {
-    if (p.B > 32) keep = b0 + lane < p.B ? tiles_of(p, cache_len(p.lens, b0 + lane, p.N), t_hi) : 0;
+    if (p.B > 32) keep = b0 + lane < p.B ? tiles_of(p, cache_len(p.lens, b0 + lane, p.N), t_hi) + extra : 0;
     int sum = keep;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
@@ -102,34 +103,39 @@ __device__ __forceinline__ int tiles_per_cta(int total, int groups) {
   return static_cast<int>((static_cast<unsigned>(total) + groups - 1) / groups);
 }
 
-// The (batch, head) pairs of a CTA's range, one after the other.
+// The (batch, head) pairs of a CTA's range, one after the other, with the tiles
+// [t0, t1) of each.
 struct Walk {
   int b, g, t0, t1, len, nt;
-  int left;  // tiles of the range not yet given out
-  __device__ __forceinline__ Walk(const TreeParams& p, int t_hi, const Start& s, int count) {
+  int left;  // of the range not yet given out
+  bool more;
+  __device__ __forceinline__ Walk(const TreeParams& p, int t_hi, int extra, const Start& s, int count) {
     left = count;
     b = s.b;
     len = cache_len(p.lens, b, p.N);
     nt = tiles_of(p, len, t_hi);
     const int in = s.begin - s.before;
-    g = in / nt;
-    t0 = in - g * nt;
-    t1 = min(nt, t0 + left);
-    left -= t1 - t0;
+    g = in / (nt + extra);
+    more = take(in - g * (nt + extra), extra) || next(p, t_hi, extra);
+  }
+  // The pair's part of the range from place v of the pair on; false when it holds no tile.
+  __device__ __forceinline__ bool take(int v, int extra) {
+    const int v1 = min(nt + extra, v + left);
+    left -= v1 - v;
+    t0 = max(v - extra, 0);
+    t1 = max(v1 - extra, 0);
+    return t1 > t0;
   }
   // The next pair; false at the range's end.
-  __device__ __forceinline__ bool next(const TreeParams& p, int t_hi) {
-    if (left <= 0) return false;
+  __device__ __forceinline__ bool next(const TreeParams& p, int t_hi, int extra) {
+    if (left <= 0) return more = false;
     if (++g == p.Hkv) {
       g = 0;
       ++b;
       len = cache_len(p.lens, b, p.N);
       nt = tiles_of(p, len, t_hi);
     }
-    t0 = 0;
-    t1 = min(nt, left);
-    left -= t1;
-    return true;
+    return more = take(0, extra);  // (only the range's last pair can hold no tile)
   }
 };
 
@@ -147,17 +153,17 @@ struct Cfg {
   static constexpr int kUnits = D == 256 ? 2 : 1;       // ring units of a K (or V) tile
   static constexpr int kUnit = (D == 64 ? 1 : 2) * kChunk;
   static constexpr int kPBytes = (NR + 63) / 64 * kChunk;
-  static constexpr int kPBufs = NR * D >= 128 * 128 ? 1 : 2;
+  static constexpr int kPBufs = D == 256 && NR == 64 ? 1 : 2;
   static constexpr int kRingK = D == 64 ? 4 : 2;
   static constexpr int kRingV = D == 64 ? 4 : (NR == 128 ? 2 : 3);
   static constexpr int kRing = kRingK + kRingV;         // K's slots first
+  static constexpr int kExtra = D == 256 ? 1 : D == 64 ? 4 : 2;  // see find_start
   static constexpr int kQ = 0;                          // NR rows x 128 B per 64 columns
   static constexpr int kQBytes = NR * D * 2;
   static constexpr int kRing0 = (kQBytes + 1023) / 1024 * 1024;
   static constexpr int kP = kRing0 + kRing * kUnit;     // behind the ring: D = 64 reads one chunk past its last unit
   static constexpr int kMisc = kP + kPBufs * kPBytes;
-  static constexpr int kMiscBytes = NR * 14 + 16 * kCols * kGroups + 256;
-  static constexpr int kBytes = kMisc + kMiscBytes + 1024;  // + slack for 1024-byte alignment
+  static constexpr int kBytes = kMisc + NR * 18 + 256;
   static constexpr int kO = 2 * NR;                     // TMEM columns: S0 [0, NR) S1 [NR, 2 NR) O [2 NR, (2 + kUnits) NR)
   static constexpr int kTmem = 4 * NR;
   static_assert(D != 256 || NR <= 64, "Q and P leave no room for the ring");
@@ -204,11 +210,10 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float (&x)[C]) {
   }
 }
 
-// Sums v[c] over the warp's lanes: in five halvings lane l ends with the sums
-// of the C / 32 (or, repeated, one) values number first + ...; returns first.
-template <int C>
-__device__ __forceinline__ int warp_sum_spread(float (&v)[C], int lane) {
-  int first = 0;
+// Reduces v[c] over the warp's lanes: lane l ends with the result of column l
+// (C = 16: l / 2) in v[0], by halvings that hand half of the columns on.
+template <int C, typename Op>
+__device__ __forceinline__ float warp_reduce_spread(float (&v)[C], int lane, Op op) {
   int n = C;
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) {
@@ -219,15 +224,14 @@ __device__ __forceinline__ int warp_sum_spread(float (&v)[C], int lane) {
       for (int c = 0; c < C / 2; ++c) {
         if (c < n) {
           const float give = up ? v[c] : v[c + n], keep = up ? v[c + n] : v[c];
-          v[c] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+          v[c] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
         }
       }
-      first += up ? n : 0;
     } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], w));
     }
   }
-  return first;
+  return v[0];
 }
 
 template <int D, int NR>
@@ -236,16 +240,15 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
                     const __grid_constant__ TreeParams p) {
   using C = Cfg<D, NR>;
   constexpr int U = C::kUnits, RK = C::kRingK, RV = C::kRingV, RING = C::kRing, PB = C::kPBufs, W = C::kCols;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rt = blockIdx.x % p.rtiles, cta = blockIdx.x / p.rtiles;
 
   float* sNegM = reinterpret_cast<float*>(smem + C::kMisc);  // [NR] minus the row's maximum; 0 while it has none
   float* sDelta = sNegM + NR;                                // [NR] what the row's outputs are multiplied by
   float* sAlpha = sDelta + NR;                               // [NR] what its sums are multiplied by as its maximum moves
-  float* sRed = sAlpha + NR;                                 // [groups][4][W] maxima, sums of the warps
-  uint8_t* sSet = reinterpret_cast<uint8_t*>(sRed + 4 * NR);  // [NR] the row has a maximum
+  float* sRed = sAlpha + NR;                                 // [NR] with sDelta and sAlpha: what warps 1 to 3 of a group hand to warp 0
+  uint8_t* sSet = reinterpret_cast<uint8_t*>(sRed + NR);     // [NR] the row has a maximum
   uint8_t* sPoison = sSet + NR;                              // [NR] the row sees a value that is not finite
   uint64_t* bars = reinterpret_cast<uint64_t*>(sPoison + NR);
   uint64_t* full = bars;               // [RING]
@@ -263,9 +266,11 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   // The merging kernel may be scheduled now: it waits for this grid to end.
   asm volatile("griddepcontrol.launch_dependents;");
   const int t_hi = last_node<NR>(p, rt);
-  const Start start = find_start(p, t_hi, [&](int total) { return cta * tiles_per_cta(total, p.groups); });
-  if (start.b < 0) return;  // more CTAs than tiles
-  const int total = min(tiles_per_cta(start.total, p.groups), start.total - start.begin);
+  constexpr int X = C::kExtra;
+  const Start start = find_start(p, t_hi, X, [&](int total) { return cta * tiles_per_cta(total, p.groups); });
+  if (start.b < 0) return;  // more CTAs than places
+  Walk w(p, t_hi, X, start, min(tiles_per_cta(start.total, p.groups), start.total - start.begin));
+  if (!w.more) return;      // none of them a tile
   if (threadIdx.x == 0) {
     for (int i = 0; i < RING; ++i) {
       mbar_init(&full[i], 1);
@@ -290,7 +295,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  Walk w(p, t_hi, start, total);
   const uint32_t ring = smem_u32(smem + C::kRing0);
 
   if (warp == C::kSoftWarps + 2) {
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
           }
           idx += U;
         }
-      } while (ok && w.next(p, t_hi));
+      } while (ok && w.next(p, t_hi, X));
       if (*s_abort) {
         // Loads in flight land before the CTA exits.
         volatile int no_abort = 0;
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         umma_commit(&s_full[n & 1]);
       }
       ++seg;
-    } while (ok && w.next(p, t_hi));
+    } while (ok && w.next(p, t_hi, X));
     umma_commit(&drain[0]);
     volatile int no_abort = 0;
     mbar_wait(&drain[0], 0, &no_abort);
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         }
         umma_commit(&p_empty[n % PB]);
       }
-    } while (ok && w.next(p, t_hi));
+    } while (ok && w.next(p, t_hi, X));
     umma_commit(&drain[1]);
     volatile int no_abort = 0;
     mbar_wait(&drain[1], 0, &no_abort);
@@ -399,30 +403,36 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     float* negM = sNegM + col0;
     float* delta = sDelta + col0;
     float* alpha = sAlpha + col0;
-    float* red = sRed + 4 * col0;
+    // Row col0 + c's slot of warp `quad` (1 to 3).
+    float* slot = (quad == 1 ? sRed : quad == 2 ? sDelta : sAlpha) + col0;
+    const float* red = sRed + col0;
     // Q of a pair, zeros for rows that are none. (A padding row's Q may be
     // anything: it reaches no other row.)
-    auto load_q = [&](int b, int g) {
-      constexpr int kPer = NR * (D / 8) / (C::kSoftWarps * 32), kStep = C::kSoftWarps * 32 / (D / 8);
-      const int u = threadIdx.x % (D / 8), r0 = threadIdx.x / (D / 8);
-      const __nv_bfloat16* src = p.q + b * p.qs[0] + static_cast<int64_t>(g) * p.G * p.qs[1] + u * 8;
-      uint4 x[kPer];
+    constexpr int kPer = NR * (D / 8) / (C::kSoftWarps * 32), kStep = C::kSoftWarps * 32 / (D / 8);
+    const int qu = threadIdx.x % (D / 8), qr = threadIdx.x / (D / 8);
+    auto fetch_q = [&](int b, int g, uint4 (&y)[kPer]) {
+      const __nv_bfloat16* src = p.q + b * p.qs[0] + static_cast<int64_t>(g) * p.G * p.qs[1] + qu * 8;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const int row = rt * NR + r0 + k * kStep;
+        const int row = rt * NR + qr + k * kStep;
         const int t = row / p.G, h = row - t * p.G;
-        x[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < p.R) x[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
+        y[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < p.R) y[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
       }
+    };
+    auto store_q = [&](const uint4 (&y)[kPer]) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const int r = r0 + k * kStep;
-        *reinterpret_cast<uint4*>(smem + C::kQ + (u >> 3) * (NR * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x[k];
+        const int r = qr + k * kStep;
+        *reinterpret_cast<uint4*>(smem + C::kQ + (qu >> 3) * (NR * 128) + r * 128 + (((qu & 7) ^ (r & 7)) << 4)) = y[k];
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     };
-    load_q(w.b, w.g);
+    constexpr bool kEarlyQ = NR < 128;  // (where the registers allow it)
+    uint4 qy[kPer];
+    fetch_q(w.b, w.g, qy);
+    store_q(qy);
     int n = 0;
     bool more;
     do {
@@ -443,9 +453,12 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 #pragma unroll
       for (int c = 0; c < W / 2; ++c) l[c] = 0ull;
 
+      Walk nx = w;
+      more = nx.next(p, t_hi, X);
       for (int t = w.t0; t < w.t1; ++t, ++n) {
         const int base = t * kKeys;
         const uint32_t st = tm + (n & 1) * NR;  // the scores
+        if (kEarlyQ && more && t == w.t1 - 1) fetch_q(nx.b, nx.g, qy);
         uint8_t* pbuf = smem + C::kP + (n % PB) * C::kPBytes;
         mbar_wait(&s_full[n & 1], (n >> 1) & 1, s_abort);
         tc_fence_after();
@@ -471,9 +484,10 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
           }
           // V of a key that is not before the sequence's end must be finite,
           // seen or not: 0 * inf would reach every row. (These threads have not
-          // followed the V ring's phases: with the last P.V done, every
-          // earlier phase of the slot is over.)
-          if (n > 0) mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
+          // followed the V ring's phases. Its slot's last unit is over when the P.V
+          // that read it is done: three tiles back, awaited for P's buffer, or, with
+          // two units to a tile, the tile before.)
+          if (U == 2 && n > 0) mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
           uint4* vrow[U];
           bool finite = true;
           if (j >= w.len) {
@@ -535,21 +549,16 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 #pragma unroll 1
         for (bool again = false;; again = true) {
           if (renew) {
-#pragma unroll 1
-            for (int c = 0; c < W; c += 16) {
-              uint32_t y[16];
-              tmem_ld_32x32b_x16(st + c, y);
-              tmem_ld_wait();
+            tmem_ld_cols<W>(st, x);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float m = warp_max(fmaf(__uint_as_float(y[i]), p.scale_log2, negM[c + i]));
-                if (lane == i) red[quad * W + c + i] = m;
-              }
-            }
+            for (int c = 0; c < W; ++c) x[c] = fmaf(x[c], p.scale_log2, negM[c]);
+            float m = warp_reduce_spread<W>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+            if (quad > 0) slot[lane / (32 / W)] = m;  // (W = 16: two lanes write the same value)
+            if (W == 16) m = __shfl_sync(0xffffffffu, m, (lane & 15) * 2);
             named_barrier(bar, 128);
             bool moved = false;
             if (tid < W) {
-              const float m = fmaxf(fmaxf(red[tid], red[W + tid]), fmaxf(red[2 * W + tid], red[3 * W + tid]));
+              m = fmaxf(fmaxf(m, red[tid]), fmaxf(delta[tid], alpha[tid]));
               const bool set = sSet[col0 + tid] != 0;
               float d = 0.f;
               if (m > (set ? kLazy : -INFINITY)) {
@@ -621,25 +630,29 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       }
 
       // Q of the next pair now: every S of this one is done.
-      Walk nx = w;
-      more = nx.next(p, t_hi);
-      if (more) load_q(nx.b, nx.g);
+      if (more) {
+        if (!kEarlyQ) fetch_q(nx.b, nx.g, qy);
+        store_q(qy);
+      }
 
       // ---- epilogue of the pair: its output, or this CTA's part of it ----
       const bool whole = w.t0 == 0 && w.t1 == w.nt;
       const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * NR + col0;
+      float part_sum;
+      named_barrier(bar, 128);  // the last tile's alpha has been read
       {
         float v[W];
 #pragma unroll
         for (int c = 0; c < W / 2; ++c) f2_unpack(l[c], v[2 * c], v[2 * c + 1]);
-        const int f = warp_sum_spread<W>(v, lane);
-        red[quad * W + f] = v[0];  // (W = 16: two lanes write the same value)
+        part_sum = warp_reduce_spread<W>(v, lane, [](float a, float b) { return a + b; });
+        if (quad > 0) slot[lane / (32 / W)] = part_sum;
+        if (W == 16) part_sum = __shfl_sync(0xffffffffu, part_sum, (lane & 15) * 2);
       }
       named_barrier(bar, 128);
       if (tid < rows && tid < W) {
         const int tt = (row0 + tid) / p.G, h = w.g * p.G + (row0 + tid) % p.G;
         const bool dead = par && __ldg(par + tt) == -2;
-        const float sum = dead ? 0.f : (red[tid] + red[W + tid]) + (red[2 * W + tid] + red[3 * W + tid]);
+        const float sum = dead ? 0.f : (part_sum + red[tid]) + (delta[tid] + alpha[tid]);
         const float m = -negM[tid];
         // -1: no output.
         delta[tid] = sum == 0.f ? -1.f : (sPoison[col0 + tid] ? NAN : (whole ? 1.f / sum : 1.f));
@@ -720,17 +733,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
   if (r >= min(NR, p.R - rt * NR)) return;  // (SPLIT: the whole block)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The CTAs that met the pair.
+  constexpr int X = Cfg<D, NR>::kExtra;
   const int t_hi = last_node<NR>(p, rt);
   int before = 0, total = 0;
   for (int x = lane; x < p.B; x += 32) {
-    const int n = tiles_of(p, cache_len(p.lens, x, p.N), t_hi);
+    const int n = tiles_of(p, cache_len(p.lens, x, p.N), t_hi) + X;
     total += n;
     if (x < b) before += n;
   }
   total = __reduce_add_sync(0xffffffffu, total) * p.Hkv;
   before = __reduce_add_sync(0xffffffffu, before);
   const int nt = tiles_of(p, cache_len(p.lens, b, p.N), t_hi);
-  const int base = before * p.Hkv + g * nt, per = tiles_per_cta(total, p.groups);
+  const int base = before * p.Hkv + g * (nt + X) + X, per = tiles_per_cta(total, p.groups);  // of its first tile
   const int c0 = base / per, c1 = (base + nt - 1) / per;
   if (c0 == c1) return;  // written by its only CTA
   const int ns = c1 - c0 + 1;
@@ -901,7 +915,7 @@ extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, 
   if (v->B != k->B || v->H != k->H || v->N != k->N || v->D != k->D) return MFA_ERR_SHAPE_MISMATCH;
   if (out->B != q->B || out->H != q->H || out->N != q->N || out->D != q->D) return MFA_ERR_SHAPE_MISMATCH;
   if (empty) return MFA_OK;
-  if (k->B * k->H * cdiv64(k->N, kKeys) >= (int64_t(1) << 31)) return MFA_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
+  if (k->B * k->H * (cdiv64(k->N, kKeys) + 4) >= (int64_t(1) << 31)) return MFA_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
   const int64_t R = q->N * (q->H / k->H);
   const TreePlan pl = plan_tree(R, q->D);
   size_t o_bytes;
