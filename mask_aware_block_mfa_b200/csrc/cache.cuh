@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "mfa.h"
+#include "mfa_device.cuh"
 #include "mfa_internal.h"
 
 namespace mfa {
@@ -44,6 +45,100 @@ __device__ __forceinline__ uint32_t draft_errors(const int32_t* lens, const int3
   return bad ? MFA_DEVERR_BOUNDS : 0u;
 }
 
+constexpr int kKeys = 128;           // keys per tile
+constexpr int kChunk = kKeys * 128;  // bytes of 64 columns of a tile, 128-byte swizzled rows
+
+// The line that is cut among the CTAs: the tiles of all (batch, head) pairs end
+// to end, each pair's up to the key of node t_hi, with `extra` more places
+// before them for what it costs to begin and end a pair.
+struct Line {
+  const int32_t* lens;
+  int B, Hkv, N, t_hi, extra;
+  __device__ __forceinline__ int len(int b) const { return cache_len(lens, b, N); }
+  __device__ __forceinline__ int tiles(int n) const { return (min(n + t_hi + 1, N) + kKeys - 1) / kKeys; }
+};
+
+__device__ __forceinline__ int places_per_cta(int total, int ctas) {
+  return static_cast<int>((static_cast<unsigned>(total) + ctas - 1) / ctas);
+}
+
+// Where CTA `cta` of `ctas` begins, found by each warp for itself (for up to 32 batches one
+// load and two shuffle reductions, without a block barrier): the line's length, the CTA's
+// first place, the batch that holds it (-1: past the end) and the length before that batch.
+struct Start {
+  int total, begin, before, b;
+};
+__device__ __forceinline__ Start find_start(const Line& ln, int cta, int ctas) {
+  const int lane = threadIdx.x & 31;
+  Start s{0, 0, 0, -1};
+  int keep = 0;  // of batch `lane` of the last 32
+  for (int b0 = 0; b0 < ln.B; b0 += 32) {
+    keep = b0 + lane < ln.B ? ln.tiles(ln.len(b0 + lane)) + ln.extra : 0;
+    s.total += __reduce_add_sync(0xffffffffu, keep);
+  }
+  s.total *= ln.Hkv;
+  s.begin = cta * places_per_cta(s.total, ctas);
+  int done = 0;  // of the batches before
+  for (int b0 = 0; b0 < ln.B && s.b < 0; b0 += 32) {
+    if (ln.B > 32) keep = b0 + lane < ln.B ? ln.tiles(ln.len(b0 + lane)) + ln.extra : 0;
+    int sum = keep;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, w);
+      if (lane >= w) sum += o;
+    }
+    const unsigned in = __ballot_sync(0xffffffffu, s.begin < done + sum * ln.Hkv);
+    if (in) {
+      const int l = __ffs(in) - 1;
+      s.b = b0 + l < ln.B ? b0 + l : -1;
+      s.before = done + __shfl_sync(0xffffffffu, sum - keep, l) * ln.Hkv;
+    }
+    done += __shfl_sync(0xffffffffu, sum, 31) * ln.Hkv;
+  }
+  return s;
+}
+
+// The (batch, head) pairs of a CTA's range, one after the other, with the tiles
+// [t0, t1) of each.
+struct Walk {
+  int b, g, t0, t1, len, nt;
+  int left;  // of the range not yet given out
+  bool more;
+  __device__ __forceinline__ Walk(const Line& ln, const Start& s, int ctas) {
+    left = min(places_per_cta(s.total, ctas), s.total - s.begin);
+    b = s.b;
+    len = ln.len(b);
+    nt = ln.tiles(len);
+    const int in = s.begin - s.before;
+    g = in / (nt + ln.extra);
+    more = take(ln, in - g * (nt + ln.extra)) || next(ln);
+  }
+  // The pair's part of the range from place v of the pair on; false when it holds no tile.
+  __device__ __forceinline__ bool take(const Line& ln, int v) {
+    const int v1 = min(nt + ln.extra, v + left);
+    left -= v1 - v;
+    t0 = max(v - ln.extra, 0);
+    t1 = max(v1 - ln.extra, 0);
+    return t1 > t0;
+  }
+  // The next pair; false at the range's end.
+  __device__ __forceinline__ bool next(const Line& ln) {
+    if (left <= 0) return more = false;
+    if (++g == ln.Hkv) {
+      g = 0;
+      ++b;
+      len = ln.len(b);
+      nt = ln.tiles(len);
+    }
+    return more = take(ln, 0);  // (only the range's last pair can hold no tile)
+  }
+};
+
+// D[tmem] = A B^T of 128 x N, both operands in shared memory, K-major or both MN-major.
+__host__ __device__ constexpr uint32_t idesc_keys(int N, bool mn_major) {
+  return idesc_bf16_f32(128, N, mn_major) | (mn_major ? 1u << 15 : 0u);
+}
+
 // ---- host ----
 
 // A [B, H, N, D] bf16 tensor as these operators take it: D contiguous, the
@@ -60,6 +155,9 @@ inline mfa_status check_cache_tensor(const mfa_tensor* t) {
   return MFA_OK;
 }
 
+// Whether the line's places can be counted in 32 bits (with the largest `extra`).
+inline bool line_fits(const mfa_tensor* k) { return k->B * k->H * (cdiv64(k->N, kKeys) + 4) < (int64_t(1) << 31); }
+
 // The checks mfa_tree_decode and mfa_key_weights share (q and the cache k
 // already checked one by one). *empty: nothing to do.
 inline mfa_status check_draft(const mfa_tensor* q, const mfa_tensor* k, const int32_t* lens, const int32_t* parents,
@@ -72,8 +170,22 @@ inline mfa_status check_draft(const mfa_tensor* q, const mfa_tensor* k, const in
   if (parents && q->N > MFA_TREE_MAX_NODES) return MFA_ERR_UNSUPPORTED;
   if (k->N == 0 || k->N >= (int64_t(1) << 30) || q->N >= (int64_t(1) << 24) || q->H > 65535 || q->B > 65535)
     return MFA_ERR_UNSUPPORTED;
-  if (q->B * q->H * q->N >= (int64_t(1) << 31)) return MFA_ERR_UNSUPPORTED;
+  if (q->B * q->H * q->N >= (int64_t(1) << 30) || !line_fits(k)) return MFA_ERR_UNSUPPORTED;
   return MFA_OK;
+}
+
+// The tensor map of a cache tensor: boxes of 64 columns x 128 keys of one head.
+inline bool map_keys(CUtensorMap* map, const mfa_tensor* t) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(t->D), static_cast<cuuint64_t>(t->N), static_cast<cuuint64_t>(t->H),
+                        static_cast<cuuint64_t>(t->B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(t->stride[2]) * 2, static_cast<cuuint64_t>(t->stride[1]) * 2,
+                           static_cast<cuuint64_t>(t->stride[0]) * 2};
+  cuuint32_t box[4] = {64, kKeys, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace mfa

@@ -1,6 +1,13 @@
 // mfa_key_weights: the attention weight every cached key got from a call's
 // rows, w[b, g, j] = decay * w_in + sum over heads h of group g and rows t that
 // see j of row_scale[t] * exp(q_ht . k_j / sqrt(D) - lse_ht).
+//
+// S^T = K Q^T on tcgen05 as in tree decode, 128 keys by the R = T * G rows of a
+// key/value head, so that a thread holds one key's scores for 16 to 128 rows at
+// a time and adds its own key's weight: no sum crosses threads but the one
+// over row tiles. K is read once for up to 512 rows, and nothing else of size
+// is. Bound: HBM (2 D bytes per key) up to about 150 rows, beyond them the
+// 16 exponentials per clock of an SM.
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -10,57 +17,357 @@
 namespace mfa {
 namespace {
 
+constexpr int kGroups = 4;                        // softmax groups of 128 threads, a TMEM buffer each
+constexpr int kSoftThreads = kGroups * 128;
+constexpr int kThreads = kSoftThreads + 64;       // + the MMA and the TMA warp
+constexpr int kMaxRing = 8;
+constexpr int kSmem = 232448;
+
 struct KeyWeightParams {
-  int32_t B, Hq, Hkv, G, T, N;
+  int32_t B, Hq, Hkv, G, T, N, R;
+  int32_t row0, qtiles, rtiles;  // rows of this pass: row0 .., in qtiles (1, 2, 4) tiles of NR, rtiles of them with rows
+  int32_t ring, words, ctas;     // K units; 32-bit words of a row's nodes; CTAs of the line
   float scale_log2, decay;
-  const __nv_bfloat16 *q, *k;
-  int64_t qs[3], ks[3];
+  const __nv_bfloat16* q;
+  int64_t qs[3];
   const float *lse, *row_scale, *w_in;
   const int32_t *lens, *parents;
   float* w_out;
   uint32_t* err;
 };
 
-constexpr int kWarps = 8;
-
-// A warp per key; its lanes hold D / 32 elements of it each.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) mfa_key_weights_kernel(const KeyWeightParams p) {
-  constexpr int E = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = blockIdx.y, b = blockIdx.z;
-  const int len = cache_len(p.lens, b, p.N);
-  const int end = min(len + p.T, p.N);
-  const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(b) * p.T : nullptr;
-  if (blockIdx.x == 0 && g == 0) {
-    for (int t = threadIdx.x; t < p.T; t += kWarps * 32) {
-      const uint32_t e = draft_errors(p.lens, p.parents, b, t, p.T, p.N);
-      if (e) atomicOr(p.err, e);
-    }
+template <int D, int NR>
+struct Cfg {
+  static constexpr int kUnits = D == 256 ? 2 : 1;   // ring units of a K tile
+  static constexpr int kUnit = (D == 64 ? 1 : 2) * kChunk;
+  static constexpr int kQTile = NR * D * 2;         // NR rows x 128 B per 64 columns
+  static constexpr int kExtra = D == 256 ? 2 : D == 64 ? 4 : 3;
+  static constexpr int kBars = 2 * kMaxRing + 1 + 2 * kGroups + 1;
+  // Bytes besides the ring (first) and Q (next): row constants, partial sums, who sees what, barriers.
+  static constexpr int rest(int qtiles, int T, int words) {
+    return qtiles * NR * 8 + 2 * kSoftThreads * 4 + (words > 0 ? T * 4 + T * words * 4 : 0) + 16 + kBars * 8 + 16;
   }
-  for (int j = blockIdx.x * kWarps + warp; j < end; j += gridDim.x * kWarps) {
-    float k[E], acc = 0.f;
+};
+
+// Where a thread's rows come from: constants of two rows, -lse in powers of two
+// and the rows' scales.
+struct RowPair {
+  float c0, c1, r0, r1;
+};
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kThreads, 1)
+    mfa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ KeyWeightParams p) {
+  using C = Cfg<D, NR>;
+  constexpr int U = C::kUnits, X = NR < 32 ? NR : 32;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* sQ = smem + p.ring * C::kUnit;                              // [qtiles]
+  RowPair* sRow = reinterpret_cast<RowPair*>(sQ + p.qtiles * C::kQTile);  // [qtiles * NR / 2]
+  float* sPart = reinterpret_cast<float*>(sRow + p.qtiles * NR / 2);   // [2][kGroups][128]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sPart + 2 * kSoftThreads);  // [ring]
+  uint64_t* empty = full + kMaxRing;
+  uint64_t* q_full = empty + kMaxRing;
+  uint64_t* s_full = q_full + 1;         // [kGroups]
+  uint64_t* s_empty = s_full + kGroups;  // [kGroups]
+  uint64_t* drain = s_empty + kGroups;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
+  int* sPar = reinterpret_cast<int*>(s_tmem + 1);                      // [T] the tree
+  uint32_t* sSeen = reinterpret_cast<uint32_t*>(sPar + p.T);           // [T][words] the nodes each one sees
+
+  const Line ln{p.lens, p.B, p.Hkv, p.N, p.T - 1, C::kExtra};
+  const Start start = find_start(ln, blockIdx.x, p.ctas);
+  if (start.b < 0) return;  // more CTAs than places
+  Walk w(ln, start, p.ctas);
+  if (!w.more) return;      // none of them a tile
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.ring; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kGroups; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 128);
+    }
+    mbar_init(q_full, kSoftThreads);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kGroups * 4) {
+    tmem_alloc(s_tmem, kGroups * NR);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp == kGroups * 4 + 1) {
+    // =================== TMA producer ===================
+    if (lane == 0) {
+      int slot = 0, round = 0;  // of the next unit
+      bool ok = true;
+      do {
+        for (int t = w.t0; t < w.t1 && ok; ++t) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) k[e] = __bfloat162float(p.k[b * p.ks[0] + g * p.ks[1] + j * p.ks[2] + lane * E + e]);
-    for (int t = 0; t < p.T; ++t) {
-      const float r = p.row_scale ? p.row_scale[static_cast<int64_t>(b) * p.T + t] : 1.f;
-      if (r == 0.f || (par && par[t] == -2) || (j >= len && !tree_sees(par, t, j - len))) continue;
-      for (int h = g * p.G; h < (g + 1) * p.G; ++h) {
-        float s = 0.f;
+          for (int u = 0; u < U; ++u) {
+            if (round > 0 && !(ok = mbar_wait(&empty[slot], (round - 1) & 1, s_abort))) break;
+            mbar_arrive_expect_tx(&full[slot], C::kUnit);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          s = fmaf(k[e], __bfloat162float(p.q[b * p.qs[0] + h * p.qs[1] + t * p.qs[2] + lane * E + e]), s);
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        const float lse = p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.T + t];
-        if (lse != -INFINITY) acc = fmaf(r, exp2f(s * p.scale_log2 - lse * 1.44269504f), acc);
+            for (int c = 0; c < C::kUnit / kChunk; ++c)
+              tma_load_4d(smem + slot * C::kUnit + c * kChunk, &tm_k, &full[slot], u * 128 + c * 64, t * kKeys, w.g, w.b);
+            if (++slot == p.ring) {
+              slot = 0;
+              ++round;
+            }
+          }
+        }
+      } while (ok && w.next(ln));
+      if (*s_abort) {
+        // Loads in flight land before the CTA exits.
+        volatile int no_abort = 0;
+        for (int i = 0; i < p.ring; ++i) {
+          const int r = i < slot ? round : round - 1;  // the slot's last load
+          if (r >= 0) mbar_wait(&full[i], r & 1, &no_abort);
+        }
       }
     }
-    if (lane == 0) {
-      const int64_t at = (static_cast<int64_t>(b) * p.Hkv + g) * p.N + j;
-      p.w_out[at] = p.decay != 0.f && p.w_in ? fmaf(p.decay, p.w_in[at], acc) : acc;
-    }
+  } else if (warp == kGroups * 4) {
+    // =================== S^T = K Q^T ===================
+    // Item i = tile * qtiles + row tile goes to buffer and group i % 4.
+    constexpr uint32_t idesc = idesc_keys(NR, false);
+    const uint32_t ring = smem_u32(smem), q_addr = smem_u32(sQ);
+    bool ok = true;
+    uint32_t item = 0;
+    int slot = 0, round = 0, seg = 0;
+    do {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(q_full, seg & 1, s_abort));
+      for (int t = w.t0; t < w.t1 && ok; ++t) {
+        int s2 = slot, r2 = round;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[s2], r2 & 1, s_abort));
+          if (++s2 == p.ring) {
+            s2 = 0;
+            ++r2;
+          }
+        }
+        for (int rt = 0; rt < p.qtiles; ++rt, ++item) {
+          const int buf = item % kGroups;
+          if (rt >= p.rtiles) continue;
+          if (item >= kGroups)
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_empty[buf], (item / kGroups - 1) & 1, s_abort));
+          if (!ok) break;
+          tc_fence_after();
+          s2 = slot;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int kk = 0; kk < D / U / 16; ++kk) {
+              const uint32_t ka = ring + s2 * C::kUnit + (kk >> 2) * kChunk + (kk & 3) * 32;
+              const uint32_t qb = q_addr + rt * C::kQTile + (u * 2 + (kk >> 2)) * (NR * 128) + (kk & 3) * 32;
+              umma_ss(tmem + buf * NR, sdesc_sw128_lo(ka, 16), sdesc_sw128_lo(qb, 16), idesc, u + kk > 0 ? 1u : 0u);
+            }
+            if (++s2 == p.ring) s2 = 0;
+          }
+          umma_commit(&s_full[buf]);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          umma_commit(&empty[slot]);
+          if (++slot == p.ring) {
+            slot = 0;
+            ++round;
+          }
+        }
+      }
+      ++seg;
+    } while (ok && w.next(ln));
+    umma_commit(drain);
+    volatile int no_abort = 0;
+    mbar_wait(drain, 0, &no_abort);
+  } else {
+    // =================== weights: a thread per key ===================
+    // A failed wait raises *s_abort and the thread runs on (every later wait
+    // then fails at once): the barriers below need all threads.
+    const int grp = warp >> 2, tid = threadIdx.x & 127;
+    const int rt = grp & (p.qtiles - 1), nn = kGroups / p.qtiles;  // the group's row tile; tiles in flight
+    const uint32_t st = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + grp * NR;
+    int n = 0;           // tiles of the CTA so far
+    int k = 0;           // of them the group's
+    do {
+      const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
+      // ---- the pair's rows (all of the last pair's S and sums are done) ----
+      // Rows that count for nothing, whatever they hold, become Q = 0 with weight 0.
+      for (int i = threadIdx.x; i < p.qtiles * NR; i += kSoftThreads) {
+        const int row = p.row0 + i;
+        float c = -INFINITY, r = 0.f;
+        if (row < p.R) {
+          const int t = row / p.G, h = w.g * p.G + row % p.G;
+          const float lse = __ldg(p.lse + (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t);
+          if (p.row_scale) r = __ldg(p.row_scale + static_cast<int64_t>(w.b) * p.T + t);
+          else r = 1.f;
+          if (lse == -INFINITY || (par && __ldg(par + t) == -2)) r = 0.f;
+          if (r != 0.f) c = lse * -1.4426950408889634f;
+        }
+        reinterpret_cast<float*>(sRow)[(i >> 1) * 4 + (i & 1)] = c;
+        reinterpret_cast<float*>(sRow)[(i >> 1) * 4 + 2 + (i & 1)] = r;
+      }
+      if (par && w.t1 * kKeys > w.len)
+        for (int i = threadIdx.x; i < p.T; i += kSoftThreads) sPar[i] = __ldg(par + i);
+      if (p.row0 == 0 && w.g == 0 && w.t0 == 0) {
+        for (int t = threadIdx.x; t < (par ? p.T : 1); t += kSoftThreads) {
+          const uint32_t e = draft_errors(p.lens, p.parents, w.b, t, p.T, p.N);
+          if (e) atomicOr(p.err, e);
+        }
+      }
+      named_barrier(1, kSoftThreads);
+      if (par && w.t1 * kKeys > w.len) {
+        for (int t = threadIdx.x; t < p.T; t += kSoftThreads) {
+          for (int x = 0; x < p.words; ++x) sSeen[t * p.words + x] = 0u;
+          for (int a = sPar[t] == -2 ? -1 : t; a >= 0; a = tree_up(sPar, a)) sSeen[t * p.words + (a >> 5)] |= 1u << (a & 31);
+        }
+      }
+      {
+        const int u = threadIdx.x % (D / 8);
+        const __nv_bfloat16* src = p.q + w.b * p.qs[0] + static_cast<int64_t>(w.g) * p.G * p.qs[1] + u * 8;
+#pragma unroll 4
+        for (int i = threadIdx.x / (D / 8); i < p.qtiles * NR; i += kSoftThreads / (D / 8)) {
+          const int row = p.row0 + i, r = i % NR;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (reinterpret_cast<const float*>(sRow)[(i >> 1) * 4 + 2 + (i & 1)] != 0.f) {
+            const int t = row / p.G, h = row - t * p.G;
+            x = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
+          }
+          *reinterpret_cast<uint4*>(sQ + (i / NR) * C::kQTile + (u >> 3) * (NR * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+      named_barrier(1, kSoftThreads);  // sSeen is complete
+
+      const int64_t out0 = (static_cast<int64_t>(w.b) * p.Hkv + w.g) * p.N;
+      const int end = min(w.len + p.T, p.N);
+      for (int t = w.t0; t < w.t1; ++t, ++n) {
+        if (n % nn != grp / p.qtiles) continue;
+        const int j = t * kKeys + tid, node = j - w.len;
+        const bool mine = rt == 0 && j < end, add = p.w_in != nullptr && p.decay != 0.f;
+        float old = 0.f;
+        if (mine && add) old = p.w_in[out0 + j];
+        uint64_t acc[2] = {0ull, 0ull};
+        if (rt < p.rtiles) {
+          mbar_wait(&s_full[grp], k & 1, s_abort);
+          tc_fence_after();
+          const RowPair* row = sRow + rt * (NR / 2);
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+          const bool draft = t * kKeys + kKeys > w.len;
+          if (!draft) {
+#pragma unroll 1
+            for (int c = 0; c < NR; c += X) {
+              uint32_t x[X];
+              if constexpr (X == 16) tmem_ld_32x32b_x16(st + c, x);
+              else tmem_ld_32x32b_x32(st + c, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < X; i += 2) {
+                const ulonglong2 cr = *reinterpret_cast<const ulonglong2*>(row + (c + i) / 2);
+                float a, b;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, cr.x), a, b);
+                acc[(i >> 1) & 1] = f2_fma(f2_pack(ex2_approx(a), ex2_approx(b)), cr.y, acc[(i >> 1) & 1]);
+              }
+            }
+          } else {
+            // Drafted keys: a thread leaves out the rows that do not see its own.
+            int tt = (p.row0 + rt * NR) / p.G, hh = (p.row0 + rt * NR) % p.G;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < NR; c += 16) {
+              uint32_t x[16];
+              tmem_ld_32x32b_x16(st + c, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                bool see = tt < p.T;
+                if (see && j >= w.len) see = j < end && (par ? (sSeen[tt * p.words + (node >> 5)] >> (node & 31)) & 1 : node <= tt);
+                const float cc = reinterpret_cast<const float*>(row)[((c + i) >> 1) * 4 + (i & 1)];
+                const float rr = reinterpret_cast<const float*>(row)[((c + i) >> 1) * 4 + 2 + (i & 1)];
+                if (see && rr != 0.f) sum = fmaf(ex2_approx(fmaf(__uint_as_float(x[i]), p.scale_log2, cc)), rr, sum);
+                if (++hh == p.G) {
+                  hh = 0;
+                  ++tt;
+                }
+              }
+            }
+            acc[0] = f2_pack(sum, 0.f);
+          }
+          tc_fence_before();
+          mbar_arrive(&s_empty[grp]);
+        }
+        const uint64_t both = f2_add(acc[0], acc[1]);
+        float lo, hi;
+        f2_unpack(both, lo, hi);
+        float sum = lo + hi;
+        if (p.qtiles > 1) {
+          // The row tiles' sums, in their order. (The barrier of the next tile is
+          // passed only once these have been read: two buffers suffice.)
+          float* part = sPart + (k & 1) * kSoftThreads;
+          if (rt > 0) part[grp * 128 + tid] = sum;
+          named_barrier(2 + grp / p.qtiles, p.qtiles * 128);
+          if (rt == 0)
+            for (int x = 1; x < p.rtiles; ++x) sum += part[(grp + x) * 128 + tid];
+        }
+        if (mine) p.w_out[out0 + j] = add ? fmaf(p.decay, old, sum) : sum;
+        ++k;
+      }
+      named_barrier(1, kSoftThreads);  // every sum of the pair is done
+    } while (w.next(ln));
+    if (*s_abort && threadIdx.x == 0) atomicOr(p.err, MFA_DEVERR_TIMEOUT);
   }
+  __syncthreads();
+  if (warp == kGroups * 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kGroups * NR);
+  }
+}
+
+// ---- host ----
+
+template <int D, int NR>
+mfa_status launch_weights(const CUtensorMap& mk, KeyWeightParams p, cudaStream_t s) {
+  using C = Cfg<D, NR>;
+  static std::atomic<uint64_t> attr_devs{0};
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(mfa_key_weights_kernel<D, NR>), kSmem, attr_devs)) return MFA_ERR_CUDA;
+  p.words = p.parents ? (p.T + 31) / 32 : 0;
+  const int sms = device_sm_count();
+  p.ctas = sms > 0 ? sms : 148;
+  for (p.row0 = 0; p.row0 < p.R; p.row0 += p.qtiles * NR) {
+    // As many rows in one pass as shared memory holds beside a ring of two tiles.
+    const int left = static_cast<int>(cdiv64(p.R - p.row0, NR));
+    p.qtiles = left >= 3 ? 4 : left;
+    auto units = [&](int q) { return (kSmem - q * C::kQTile - C::rest(q, p.T, p.words)) / C::kUnit; };
+    while (p.qtiles > 1 && units(p.qtiles) < 2 * C::kUnits) p.qtiles /= 2;
+    p.rtiles = left < p.qtiles ? left : p.qtiles;
+    p.ring = units(p.qtiles);
+    if (p.ring > kMaxRing) p.ring = kMaxRing;
+    const int bytes = p.ring * C::kUnit + p.qtiles * C::kQTile + C::rest(p.qtiles, p.T, p.words);
+    mfa_key_weights_kernel<D, NR><<<p.ctas, kThreads, bytes, s>>>(mk, p);
+    if (cudaGetLastError() != cudaSuccess) return MFA_ERR_CUDA;
+    // Later rows add to what this pass wrote.
+    p.w_in = p.w_out;
+    p.decay = 1.f;
+  }
+  return MFA_OK;
+}
+
+template <int D>
+mfa_status launch_weights_rows(const CUtensorMap& mk, const KeyWeightParams& p, cudaStream_t s) {
+  if (p.R <= 16) return launch_weights<D, 16>(mk, p, s);
+  if (p.R <= 32) return launch_weights<D, 32>(mk, p, s);
+  if (p.R <= 64) return launch_weights<D, 64>(mk, p, s);
+  return launch_weights<D, 128>(mk, p, s);
 }
 
 }  // namespace
@@ -77,23 +384,20 @@ extern "C" mfa_status mfa_key_weights(const mfa_tensor* q, const mfa_tensor* k, 
   if (q->N == 0) return MFA_ERR_UNSUPPORTED;
   if (empty) return MFA_OK;
   if (!weights_out) return MFA_ERR_INVALID_ARG;
+  CUtensorMap mk;
+  if (!map_keys(&mk, k)) return MFA_ERR_CUDA;
   KeyWeightParams p;
   p.B = static_cast<int32_t>(q->B); p.Hq = static_cast<int32_t>(q->H); p.Hkv = static_cast<int32_t>(k->H);
   p.G = static_cast<int32_t>(q->H / k->H); p.T = static_cast<int32_t>(q->N); p.N = static_cast<int32_t>(k->N);
+  p.R = p.T * p.G;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(q->D)));
   p.decay = decay;
   p.q = static_cast<const __nv_bfloat16*>(q->data);
-  p.k = static_cast<const __nv_bfloat16*>(k->data);
-  for (int a = 0; a < 3; ++a) {
-    p.qs[a] = q->stride[a]; p.ks[a] = k->stride[a];
-  }
+  for (int a = 0; a < 3; ++a) p.qs[a] = q->stride[a];
   p.lse = lse; p.row_scale = row_scale; p.w_in = weights_in; p.w_out = weights_out;
   p.lens = lens; p.parents = parents; p.err = dev_err;
-  const int64_t blocks = cdiv64(p.N, kWarps);
-  const dim3 grid(static_cast<unsigned>(blocks < 256 ? blocks : 256), p.Hkv, p.B);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (q->D == 64) mfa_key_weights_kernel<64><<<grid, kWarps * 32, 0, s>>>(p);
-  else if (q->D == 128) mfa_key_weights_kernel<128><<<grid, kWarps * 32, 0, s>>>(p);
-  else mfa_key_weights_kernel<256><<<grid, kWarps * 32, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MFA_OK : MFA_ERR_CUDA;
+  if (q->D == 64) return launch_weights_rows<64>(mk, p, s);
+  if (q->D == 128) return launch_weights_rows<128>(mk, p, s);
+  return launch_weights_rows<256>(mk, p, s);
 }

@@ -33,8 +33,6 @@
 namespace mfa {
 namespace {
 
-constexpr int kKeys = 128;           // keys per tile
-constexpr int kChunk = kKeys * 128;  // bytes of 64 columns of a tile, 128-byte swizzled rows
 constexpr int kMaxRows = 128;        // query rows per row tile
 constexpr int kSeenWords = MFA_TREE_MAX_NODES / 32;
 constexpr float kLazy = 8.0f;        // a row's maximum moves when a score exceeds it by this (in powers of two)
@@ -51,93 +49,10 @@ struct TreeParams {
   uint32_t* err;
 };
 
-// Tiles of a (batch, head) pair for row tile rt: up to the last node its rows can see.
 template <int NR>
 __device__ __forceinline__ int last_node(const TreeParams& p, int rt) {
   return min((rt * NR + NR - 1) / p.G, p.T - 1);
 }
-__device__ __forceinline__ int tiles_of(const TreeParams& p, int len, int t_hi) {
-  return (min(len + t_hi + 1, p.N) + kKeys - 1) / kKeys;
-}
-
-// The line that is cut: a pair counts its tiles and `extra` more before them, for
-// what it costs to begin and end one (Q, the first maxima, the epilogue).
-// For one warp: all lanes get the line's length and the batch that holds
-// place `at(length)`, with the length before that batch (b = -1: past the end). Every warp finds this for itself: for up to
-// 32 batches it is one load and two shuffle scans, without a block barrier.
-struct Start {
-  int total, begin, before, b;
-};
-template <typename At>
-__device__ __forceinline__ Start find_start(const TreeParams& p, int t_hi, int extra, At at) {
-  const int lane = threadIdx.x & 31;
-  Start s{0, 0, 0, -1};
-  int keep = 0;  // of batch `lane` of the last 32
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    keep = b0 + lane < p.B ? tiles_of(p, cache_len(p.lens, b0 + lane, p.N), t_hi) + extra : 0;
-    s.total += __reduce_add_sync(0xffffffffu, keep);
-  }
-  s.total *= p.Hkv;
-  s.begin = at(s.total);
-  int done = 0;  // of the batches before
-  for (int b0 = 0; b0 < p.B && s.b < 0; b0 += 32) {
-    if (p.B > 32) keep = b0 + lane < p.B ? tiles_of(p, cache_len(p.lens, b0 + lane, p.N), t_hi) + extra : 0;
-    int sum = keep;
-#pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, sum, w);
-      if (lane >= w) sum += o;
-    }
-    const unsigned in = __ballot_sync(0xffffffffu, s.begin < done + sum * p.Hkv);
-    if (in) {
-      const int l = __ffs(in) - 1;
-      s.b = b0 + l < p.B ? b0 + l : -1;
-      s.before = done + __shfl_sync(0xffffffffu, sum - keep, l) * p.Hkv;
-    }
-    done += __shfl_sync(0xffffffffu, sum, 31) * p.Hkv;
-  }
-  return s;
-}
-
-__device__ __forceinline__ int tiles_per_cta(int total, int groups) {
-  return static_cast<int>((static_cast<unsigned>(total) + groups - 1) / groups);
-}
-
-// The (batch, head) pairs of a CTA's range, one after the other, with the tiles
-// [t0, t1) of each.
-struct Walk {
-  int b, g, t0, t1, len, nt;
-  int left;  // of the range not yet given out
-  bool more;
-  __device__ __forceinline__ Walk(const TreeParams& p, int t_hi, int extra, const Start& s, int count) {
-    left = count;
-    b = s.b;
-    len = cache_len(p.lens, b, p.N);
-    nt = tiles_of(p, len, t_hi);
-    const int in = s.begin - s.before;
-    g = in / (nt + extra);
-    more = take(in - g * (nt + extra), extra) || next(p, t_hi, extra);
-  }
-  // The pair's part of the range from place v of the pair on; false when it holds no tile.
-  __device__ __forceinline__ bool take(int v, int extra) {
-    const int v1 = min(nt + extra, v + left);
-    left -= v1 - v;
-    t0 = max(v - extra, 0);
-    t1 = max(v1 - extra, 0);
-    return t1 > t0;
-  }
-  // The next pair; false at the range's end.
-  __device__ __forceinline__ bool next(const TreeParams& p, int t_hi, int extra) {
-    if (left <= 0) return more = false;
-    if (++g == p.Hkv) {
-      g = 0;
-      ++b;
-      len = cache_len(p.lens, b, p.N);
-      nt = tiles_of(p, len, t_hi);
-    }
-    return more = take(0, extra);  // (only the range's last pair can hold no tile)
-  }
-};
 
 // ---------------------------------------------------------------------------
 // Layout. K and V come in units of 128 keys x 128 columns (64 for D = 64), each
@@ -157,7 +72,7 @@ struct Cfg {
   static constexpr int kRingK = D == 64 ? 4 : 2;
   static constexpr int kRingV = D == 64 ? 4 : (NR == 128 ? 2 : 3);
   static constexpr int kRing = kRingK + kRingV;         // K's slots first
-  static constexpr int kExtra = D == 256 ? 1 : D == 64 ? 4 : 2;  // see find_start
+  static constexpr int kExtra = D == 256 ? 1 : D == 64 ? 4 : 2;  // see Line
   static constexpr int kQ = 0;                          // NR rows x 128 B per 64 columns
   static constexpr int kQBytes = NR * D * 2;
   static constexpr int kRing0 = (kQBytes + 1023) / 1024 * 1024;
@@ -170,11 +85,6 @@ struct Cfg {
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(kTmem <= 512, "TMEM columns");
 };
-
-// D[tmem] = A B^T with both operands in shared memory; A and B K-major or both MN-major.
-__host__ __device__ constexpr uint32_t idesc_tree(int N, bool mn_major) {
-  return idesc_bf16_f32(128, N, mn_major) | (mn_major ? 1u << 15 : 0u);
-}
 
 __device__ __forceinline__ bool vote_or(uint32_t id, bool x) {
   uint32_t r;
@@ -265,11 +175,10 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 
   // The merging kernel may be scheduled now: it waits for this grid to end.
   asm volatile("griddepcontrol.launch_dependents;");
-  const int t_hi = last_node<NR>(p, rt);
-  constexpr int X = C::kExtra;
-  const Start start = find_start(p, t_hi, X, [&](int total) { return cta * tiles_per_cta(total, p.groups); });
+  const Line ln{p.lens, p.B, p.Hkv, p.N, last_node<NR>(p, rt), C::kExtra};
+  const Start start = find_start(ln, cta, p.groups);
   if (start.b < 0) return;  // more CTAs than places
-  Walk w(p, t_hi, X, start, min(tiles_per_cta(start.total, p.groups), start.total - start.begin));
+  Walk w(ln, start, p.groups);
   if (!w.more) return;      // none of them a tile
   if (threadIdx.x == 0) {
     for (int i = 0; i < RING; ++i) {
@@ -321,7 +230,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
           }
           idx += U;
         }
-      } while (ok && w.next(p, t_hi, X));
+      } while (ok && w.next(ln));
       if (*s_abort) {
         // Loads in flight land before the CTA exits.
         volatile int no_abort = 0;
@@ -331,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     }
   } else if (warp == C::kSoftWarps) {
     // =================== S^T = K Q^T ===================
-    constexpr uint32_t idesc = idesc_tree(NR, false);
+    constexpr uint32_t idesc = idesc_keys(NR, false);
     const uint32_t q_addr = smem_u32(smem + C::kQ);
     bool ok = true;
     int n = 0, seg = 0;
@@ -356,13 +265,13 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         umma_commit(&s_full[n & 1]);
       }
       ++seg;
-    } while (ok && w.next(p, t_hi, X));
+    } while (ok && w.next(ln));
     umma_commit(&drain[0]);
     volatile int no_abort = 0;
     mbar_wait(&drain[0], 0, &no_abort);
   } else if (warp == C::kSoftWarps + 1) {
     // =================== O^T += V^T P^T ===================
-    constexpr uint32_t idesc = idesc_tree(NR, true);
+    constexpr uint32_t idesc = idesc_keys(NR, true);
     bool ok = true;
     int n = 0;
     do {
@@ -384,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         }
         umma_commit(&p_empty[n % PB]);
       }
-    } while (ok && w.next(p, t_hi, X));
+    } while (ok && w.next(ln));
     umma_commit(&drain[1]);
     volatile int no_abort = 0;
     mbar_wait(&drain[1], 0, &no_abort);
@@ -454,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       for (int c = 0; c < W / 2; ++c) l[c] = 0ull;
 
       Walk nx = w;
-      more = nx.next(p, t_hi, X);
+      more = nx.next(ln);
       for (int t = w.t0; t < w.t1; ++t, ++n) {
         const int base = t * kKeys;
         const uint32_t st = tm + (n & 1) * NR;  // the scores
@@ -733,18 +642,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
   if (r >= min(NR, p.R - rt * NR)) return;  // (SPLIT: the whole block)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The CTAs that met the pair.
-  constexpr int X = Cfg<D, NR>::kExtra;
-  const int t_hi = last_node<NR>(p, rt);
+  const Line ln{p.lens, p.B, p.Hkv, p.N, last_node<NR>(p, rt), Cfg<D, NR>::kExtra};
   int before = 0, total = 0;
   for (int x = lane; x < p.B; x += 32) {
-    const int n = tiles_of(p, cache_len(p.lens, x, p.N), t_hi) + X;
+    const int n = ln.tiles(ln.len(x)) + ln.extra;
     total += n;
     if (x < b) before += n;
   }
   total = __reduce_add_sync(0xffffffffu, total) * p.Hkv;
   before = __reduce_add_sync(0xffffffffu, before);
-  const int nt = tiles_of(p, cache_len(p.lens, b, p.N), t_hi);
-  const int base = before * p.Hkv + g * (nt + X) + X, per = tiles_per_cta(total, p.groups);  // of its first tile
+  const int nt = ln.tiles(ln.len(b));
+  const int base = before * p.Hkv + g * (nt + ln.extra) + ln.extra;  // of its first tile
+  const int per = places_per_cta(total, p.groups);
   const int c0 = base / per, c1 = (base + nt - 1) / per;
   if (c0 == c1) return;  // written by its only CTA
   const int ns = c1 - c0 + 1;
@@ -839,19 +748,6 @@ size_t part_bytes(const TreePlan& pl, int64_t D, size_t* o_bytes) {
   return *o_bytes + align256(rows * 2 * 4) + 256;
 }
 
-bool map_keys(CUtensorMap* map, const mfa_tensor* t) {
-  auto fn = tensor_map_encoder();
-  if (!fn) return false;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(t->D), static_cast<cuuint64_t>(t->N), static_cast<cuuint64_t>(t->H),
-                        static_cast<cuuint64_t>(t->B)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(t->stride[2]) * 2, static_cast<cuuint64_t>(t->stride[1]) * 2,
-                           static_cast<cuuint64_t>(t->stride[0]) * 2};
-  cuuint32_t box[4] = {64, kKeys, 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, int NR>
 mfa_status launch_tree(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
   using C = Cfg<D, NR>;
@@ -915,7 +811,6 @@ extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, 
   if (v->B != k->B || v->H != k->H || v->N != k->N || v->D != k->D) return MFA_ERR_SHAPE_MISMATCH;
   if (out->B != q->B || out->H != q->H || out->N != q->N || out->D != q->D) return MFA_ERR_SHAPE_MISMATCH;
   if (empty) return MFA_OK;
-  if (k->B * k->H * (cdiv64(k->N, kKeys) + 4) >= (int64_t(1) << 31)) return MFA_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
   const int64_t R = q->N * (q->H / k->H);
   const TreePlan pl = plan_tree(R, q->D);
   size_t o_bytes;

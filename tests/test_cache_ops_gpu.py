@@ -367,6 +367,38 @@ def test_key_weights_match_the_oracle(case):
         assert torch.equal(acc.cpu(), want)
 
 
+@pytest.mark.parametrize("D,G,T,tree", [(64, 2, 2, None), (64, 4, 32, "random"), (64, 4, 100, "random"), (128, 2, 1, None), (128, 4, 7, "random"),
+                                        (128, 5, 10, "random"), (128, 4, 30, "random"), (128, 4, 50, "random"), (128, 4, 80, "random"),
+                                        (128, 4, 120, "random"), (128, 16, 40, "random"), (256, 2, 3, None), (256, 4, 8, "random"),
+                                        (256, 4, 30, "random"), (256, 8, 30, "random")])
+def test_key_weights_with_many_tiles_and_pairs_per_block(D, G, T, tree):
+    """As for tree decode; 2 to 640 rows: one to four row tiles at once, one or two passes."""
+    lens = [9000, 40, 0, 5117, 300, 9728 - T, 128]
+    q, k, v, lens, parents = make(D + T, len(lens), 8 * G, 8, T, 9728, D, lens, tree, True)
+    args = [to_gpu(x) for x in (q, k, k, lens, parents)]
+    _, lse = reference(args, D)
+    lse = lse.float()
+    gen = torch.Generator().manual_seed(3)
+    old = torch.rand(len(lens), 8, 9728, generator=gen).cuda()
+    row = (torch.rand(len(lens), T, generator=gen) < 0.6).float().cuda()
+    kw = B.KeyWeights()
+    runs = [kw(args[0], args[1], lse, args[3], args[4], row, old, 0.5, torch.full_like(old, 7.0)) for _ in range(3)]
+    assert kw.status() == 0 and torch.equal(runs[0], runs[1]) and torch.equal(runs[0], runs[2])
+    want = torch.full_like(old, 7.0).double()
+    for b in range(len(lens)):
+        end = int(lens[b]) + T
+        vis = torch.from_numpy(OT.visible(int(lens[b]), None if parents is None else parents[b].tolist(), T, 9728)[:, :end]).cuda()
+        s = args[0][b].double() @ args[1][b, :, :end].double().repeat_interleave(G, 0).transpose(1, 2) / math.sqrt(D)
+        p = torch.where(vis, (s - lse[b].double()[..., None]).exp(), 0.0) * row[b].double()[None, :, None]
+        want[b, :, :end] = p.view(8, G * T, end).sum(1) + 0.5 * old[b, :, :end].double()
+    # every term is positive: the roundings of weights_tolerance, with |q . k| bounded by |q| |k|
+    rows = T * G
+    ds = float((D + 4) * ULP * args[0].double().norm(dim=-1).max() * args[1].double().norm(dim=-1).max() / math.sqrt(D))
+    top = float(lse[torch.isfinite(lse)].abs().max())
+    tol = want.abs() * (ds + 2 * ULP * (top + 64) + (rows + 8) * ULP) + rows * math.exp(-64)
+    assert ((runs[0].double() - want).abs() <= tol).all()
+
+
 def test_key_weights_leave_out_what_rows_of_scale_zero_hold():
     q, k, v, lens, parents = make(30, 1, 4, 2, 6, 300, 128, [280], [[-1, 0, 0, 1, 2, -2]])
     _, lse, _ = decode(q, k, v, lens, parents)
