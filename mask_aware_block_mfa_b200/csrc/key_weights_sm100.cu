@@ -5,9 +5,15 @@
 // S^T = K Q^T on tcgen05 as in tree decode, 128 keys by the R = T * G rows of a
 // key/value head, so that a thread holds one key's scores for 16 to 128 rows at
 // a time and adds its own key's weight: no sum crosses threads but the one
-// over row tiles. K is read once for up to 512 rows, and nothing else of size
+// over row tiles. K is read once for up to 256 rows, and nothing else of size
 // is. Bound: HBM (2 D bytes per key) up to about 150 rows, beyond them the
 // 16 exponentials per clock of an SM.
+//
+// What a row adds to every score, -lse and the logarithm of its scale's size, would cost
+// each thread a shared-memory read per row (as much of the SM's time as the
+// exponentials); it comes out of the tensor core instead, as 16 more products
+// per score: ones for the key times the constant in three bf16 parts, which
+// hold a float32's 24 bits, added after the D others so that they are not rounded at its size.
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -25,7 +31,7 @@ constexpr int kSmem = 232448;
 
 struct KeyWeightParams {
   int32_t B, Hq, Hkv, G, T, N, R;
-  int32_t row0, qtiles, rtiles;  // rows of this pass: row0 .., in qtiles (1, 2, 4) tiles of NR, rtiles of them with rows
+  int32_t row0, qtiles;          // rows of this pass: row0 .., in qtiles (1 or 2) tiles of NR
   int32_t ring, words, ctas;     // K units; 32-bit words of a row's nodes; CTAs of the line
   float scale_log2, decay;
   const __nv_bfloat16* q;
@@ -43,16 +49,11 @@ struct Cfg {
   static constexpr int kQTile = NR * D * 2;         // NR rows x 128 B per 64 columns
   static constexpr int kExtra = D == 256 ? 2 : D == 64 ? 4 : 3;
   static constexpr int kBars = 2 * kMaxRing + 1 + 2 * kGroups + 1;
-  // Bytes besides the ring (first) and Q (next): row constants, partial sums, who sees what, barriers.
+  static constexpr int kConst = NR * 128;           // constants of the rows: 32 bytes for each row tile
+  // Bytes besides the ring (first) and Q (next): ones, constants, signs, partial sums, who sees what, barriers.
   static constexpr int rest(int qtiles, int T, int words) {
-    return qtiles * NR * 8 + 2 * kSoftThreads * 4 + (words > 0 ? T * 4 + T * words * 4 : 0) + 16 + kBars * 8 + 16;
+    return kChunk + kConst + qtiles * NR * 4 + 2 * kSoftThreads * 4 + (words > 0 ? T * 4 + T * words * 4 : 0) + 16 + kBars * 8 + 16;
   }
-};
-
-// Where a thread's rows come from: constants of two rows, -lse in powers of two
-// and the rows' scales.
-struct RowPair {
-  float c0, c1, r0, r1;
 };
 
 template <int D, int NR>
@@ -63,8 +64,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* sQ = smem + p.ring * C::kUnit;                              // [qtiles]
-  RowPair* sRow = reinterpret_cast<RowPair*>(sQ + p.qtiles * C::kQTile);  // [qtiles * NR / 2]
-  float* sPart = reinterpret_cast<float*>(sRow + p.qtiles * NR / 2);   // [2][kGroups][128]
+  uint8_t* sOnes = sQ + p.qtiles * C::kQTile;                          // [128 keys] 1 1 1 0 ..
+  uint8_t* sConst = sOnes + kChunk;                                    // [NR]
+  float* sSign = reinterpret_cast<float*>(sConst + C::kConst);         // [qtiles * NR] of the row's scale; 0: it is left out
+  float* sPart = sSign + p.qtiles * NR;                                // [2][kGroups][128]
   uint64_t* full = reinterpret_cast<uint64_t*>(sPart + 2 * kSoftThreads);  // [ring]
   uint64_t* empty = full + kMaxRing;
   uint64_t* q_full = empty + kMaxRing;
@@ -73,7 +76,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = s_empty + kGroups;
   volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
-  int* sPar = reinterpret_cast<int*>(s_tmem + 1);                      // [T] the tree
+  int* s_minus = reinterpret_cast<int*>(s_tmem + 1);                   // a row of the pair has a negative scale
+  int* sPar = s_minus + 1;                                             // [T] the tree
   uint32_t* sSeen = reinterpret_cast<uint32_t*>(sPar + p.T);           // [T][words] the nodes each one sees
 
   const Line ln{p.lens, p.B, p.Hkv, p.N, p.T - 1, C::kExtra};
@@ -156,7 +160,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int rt = 0; rt < p.qtiles; ++rt, ++item) {
           const int buf = item % kGroups;
-          if (rt >= p.rtiles) continue;
           if (item >= kGroups)
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_empty[buf], (item / kGroups - 1) & 1, s_abort));
           if (!ok) break;
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (++s2 == p.ring) s2 = 0;
           }
+          umma_ss(tmem + buf * NR, sdesc_sw128_lo(smem_u32(sOnes), 16), sdesc_sw128_lo(smem_u32(sConst) + rt * 32, 16), idesc, 1u);
           umma_commit(&s_full[buf]);
         }
         if (!ok) break;
@@ -196,25 +200,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int grp = warp >> 2, tid = threadIdx.x & 127;
     const int rt = grp & (p.qtiles - 1), nn = kGroups / p.qtiles;  // the group's row tile; tiles in flight
     const uint32_t st = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + grp * NR;
+    for (int i = threadIdx.x; i < kKeys * 2; i += kSoftThreads) {
+      const int r = i >> 1, u = i & 1;
+      *reinterpret_cast<uint4*>(sOnes + r * 128 + ((u ^ (r & 7)) << 4)) =
+          u == 0 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+    }
     int n = 0;           // tiles of the CTA so far
     int k = 0;           // of them the group's
     do {
       const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
       // ---- the pair's rows (all of the last pair's S and sums are done) ----
-      // Rows that count for nothing, whatever they hold, become Q = 0 with weight 0.
+      // Rows that count for nothing, whatever they hold, become Q = 0 with a constant that
+      // no exponential survives.
+      if (threadIdx.x == 0) *s_minus = 0;
+      named_barrier(1, kSoftThreads);
       for (int i = threadIdx.x; i < p.qtiles * NR; i += kSoftThreads) {
-        const int row = p.row0 + i;
-        float c = -INFINITY, r = 0.f;
+        const int row = p.row0 + i, r = i % NR, q = i / NR;
+        float c = -1e30f, sign = 0.f;
         if (row < p.R) {
           const int t = row / p.G, h = w.g * p.G + row % p.G;
           const float lse = __ldg(p.lse + (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t);
-          if (p.row_scale) r = __ldg(p.row_scale + static_cast<int64_t>(w.b) * p.T + t);
-          else r = 1.f;
-          if (lse == -INFINITY || (par && __ldg(par + t) == -2)) r = 0.f;
-          if (r != 0.f) c = lse * -1.4426950408889634f;
+          const float scale = p.row_scale ? __ldg(p.row_scale + static_cast<int64_t>(w.b) * p.T + t) : 1.f;
+          if (scale != 0.f && lse != -INFINITY && !(par && __ldg(par + t) == -2)) {
+            sign = scale < 0.f ? -1.f : 1.f;
+            if (scale < 0.f) *s_minus = 1;
+            c = (log2f(fabsf(scale)) - lse * 1.4426950408889634f) / p.scale_log2;  // in the scores' unit
+          }
         }
-        reinterpret_cast<float*>(sRow)[(i >> 1) * 4 + (i & 1)] = c;
-        reinterpret_cast<float*>(sRow)[(i >> 1) * 4 + 2 + (i & 1)] = r;
+        sSign[i] = sign;
+        uint32_t part[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const __nv_bfloat16 y = __float2bfloat16_rn(c);
+          part[k] = __bfloat16_as_ushort(y);
+          c = isfinite(__bfloat162float(y)) ? c - __bfloat162float(y) : 0.f;
+        }
+        uint8_t* to = sConst + r * 128;
+        *reinterpret_cast<uint4*>(to + (((2 * q) ^ (r & 7)) << 4)) = make_uint4(part[0] | part[1] << 16, part[2], 0u, 0u);
+        *reinterpret_cast<uint4*>(to + (((2 * q + 1) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
       }
       if (par && w.t1 * kKeys > w.len)
         for (int i = threadIdx.x; i < p.T; i += kSoftThreads) sPar[i] = __ldg(par + i);
@@ -238,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = threadIdx.x / (D / 8); i < p.qtiles * NR; i += kSoftThreads / (D / 8)) {
           const int row = p.row0 + i, r = i % NR;
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (reinterpret_cast<const float*>(sRow)[(i >> 1) * 4 + 2 + (i & 1)] != 0.f) {
+          if (sSign[i] != 0.f) {
             const int t = row / p.G, h = row - t * p.G;
             x = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
           }
@@ -248,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(q_full);
       named_barrier(1, kSoftThreads);  // sSeen is complete
+      const bool minus = *s_minus != 0;
 
       const int64_t out0 = (static_cast<int64_t>(w.b) * p.Hkv + w.g) * p.N;
       const int end = min(w.len + p.T, p.N);
@@ -258,54 +282,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         float old = 0.f;
         if (mine && add) old = p.w_in[out0 + j];
         uint64_t acc[2] = {0ull, 0ull};
-        if (rt < p.rtiles) {
-          mbar_wait(&s_full[grp], k & 1, s_abort);
-          tc_fence_after();
-          const RowPair* row = sRow + rt * (NR / 2);
-          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-          const bool draft = t * kKeys + kKeys > w.len;
-          if (!draft) {
-#pragma unroll 1
-            for (int c = 0; c < NR; c += X) {
-              uint32_t x[X];
-              if constexpr (X == 16) tmem_ld_32x32b_x16(st + c, x);
-              else tmem_ld_32x32b_x32(st + c, x);
-              tmem_ld_wait();
+        mbar_wait(&s_full[grp], k & 1, s_abort);
+        tc_fence_after();
+        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+        if (t * kKeys + kKeys <= w.len && !minus) {
 #pragma unroll
-              for (int i = 0; i < X; i += 2) {
-                const ulonglong2 cr = *reinterpret_cast<const ulonglong2*>(row + (c + i) / 2);
-                float a, b;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, cr.x), a, b);
-                acc[(i >> 1) & 1] = f2_fma(f2_pack(ex2_approx(a), ex2_approx(b)), cr.y, acc[(i >> 1) & 1]);
-              }
-            }
-          } else {
-            // Drafted keys: a thread leaves out the rows that do not see its own.
-            int tt = (p.row0 + rt * NR) / p.G, hh = (p.row0 + rt * NR) % p.G;
-            float sum = 0.f;
-#pragma unroll 1
-            for (int c = 0; c < NR; c += 16) {
-              uint32_t x[16];
-              tmem_ld_32x32b_x16(st + c, x);
-              tmem_ld_wait();
+          for (int c = 0; c < NR; c += X) {
+            uint32_t x[X];
+            if constexpr (X == 16) tmem_ld_32x32b_x16(st + c, x);
+            else tmem_ld_32x32b_x32(st + c, x);
+            tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                bool see = tt < p.T;
-                if (see && j >= w.len) see = j < end && (par ? (sSeen[tt * p.words + (node >> 5)] >> (node & 31)) & 1 : node <= tt);
-                const float cc = reinterpret_cast<const float*>(row)[((c + i) >> 1) * 4 + (i & 1)];
-                const float rr = reinterpret_cast<const float*>(row)[((c + i) >> 1) * 4 + 2 + (i & 1)];
-                if (see && rr != 0.f) sum = fmaf(ex2_approx(fmaf(__uint_as_float(x[i]), p.scale_log2, cc)), rr, sum);
-                if (++hh == p.G) {
-                  hh = 0;
-                  ++tt;
-                }
-              }
+            for (int i = 0; i < X; i += 2) {
+              float a, b;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2), a, b);
+              acc[(i >> 1) & 1] = f2_add(acc[(i >> 1) & 1], f2_pack(ex2_approx(a), ex2_approx(b)));
             }
-            acc[0] = f2_pack(sum, 0.f);
           }
-          tc_fence_before();
-          mbar_arrive(&s_empty[grp]);
+        } else {
+          // Negative scales, or drafted keys: a thread leaves out the rows that do not see its own.
+          int tt = (p.row0 + rt * NR) / p.G, hh = (p.row0 + rt * NR) % p.G;
+          float sum = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < NR; c += 16) {
+            uint32_t x[16];
+            tmem_ld_32x32b_x16(st + c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              bool see = tt < p.T;
+              if (see && j >= w.len) see = j < end && (par ? (sSeen[tt * p.words + (node >> 5)] >> (node & 31)) & 1 : node <= tt);
+              const float sign = sSign[rt * NR + c + i];
+              if (see && sign != 0.f) sum = fmaf(ex2_approx(__uint_as_float(x[i]) * p.scale_log2), sign, sum);
+              if (++hh == p.G) {
+                hh = 0;
+                ++tt;
+              }
+            }
+          }
+          acc[0] = f2_pack(sum, 0.f);
         }
+        tc_fence_before();
+        mbar_arrive(&s_empty[grp]);
         const uint64_t both = f2_add(acc[0], acc[1]);
         float lo, hi;
         f2_unpack(both, lo, hi);
@@ -315,9 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // passed only once these have been read: two buffers suffice.)
           float* part = sPart + (k & 1) * kSoftThreads;
           if (rt > 0) part[grp * 128 + tid] = sum;
-          named_barrier(2 + grp / p.qtiles, p.qtiles * 128);
-          if (rt == 0)
-            for (int x = 1; x < p.rtiles; ++x) sum += part[(grp + x) * 128 + tid];
+          named_barrier(2 + grp / 2, 256);
+          if (rt == 0) sum += part[(grp + 1) * 128 + tid];
         }
         if (mine) p.w_out[out0 + j] = add ? fmaf(p.decay, old, sum) : sum;
         ++k;
@@ -344,12 +361,12 @@ mfa_status launch_weights(const CUtensorMap& mk, KeyWeightParams p, cudaStream_t
   const int sms = device_sm_count();
   p.ctas = sms > 0 ? sms : 148;
   for (p.row0 = 0; p.row0 < p.R; p.row0 += p.qtiles * NR) {
-    // As many rows in one pass as shared memory holds beside a ring of two tiles.
+    // Two row tiles in one pass where shared memory holds them beside a ring of two tiles: more
+    // would not help, as with two the exponentials already take longer than K's next read.
     const int left = static_cast<int>(cdiv64(p.R - p.row0, NR));
-    p.qtiles = left >= 3 ? 4 : left;
+    p.qtiles = left >= 2 ? 2 : 1;
     auto units = [&](int q) { return (kSmem - q * C::kQTile - C::rest(q, p.T, p.words)) / C::kUnit; };
-    while (p.qtiles > 1 && units(p.qtiles) < 2 * C::kUnits) p.qtiles /= 2;
-    p.rtiles = left < p.qtiles ? left : p.qtiles;
+    if (units(p.qtiles) < 2 * C::kUnits) p.qtiles = 1;
     p.ring = units(p.qtiles);
     if (p.ring > kMaxRing) p.ring = kMaxRing;
     const int bytes = p.ring * C::kUnit + p.qtiles * C::kQTile + C::rest(p.qtiles, p.T, p.words);
