@@ -33,6 +33,24 @@ __device__ __forceinline__ bool tree_sees(const int32_t* par, int t, int n) {
   return a == n;
 }
 
+// Which of the X rows from `first` on (row = node * G + head) see the key of `node`, as
+// bits: in a chain the rows from first + from on; in a tree by the table
+// seen[T][words] of the nodes each node sees.
+__device__ __forceinline__ uint32_t rows_from(int from) { return from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from; }
+template <int X>
+__device__ __forceinline__ uint32_t rows_seeing(const uint32_t* seen, int words, int node, int first, int G, int T) {
+  uint32_t bits = 0u;
+  const uint32_t* col = seen + (node >> 5);
+  const int t0 = first / G, t1 = min((first + X - 1) / G, T - 1);
+#pragma unroll 4
+  for (int t = t0; t <= t1; ++t) {
+    const uint32_t yes = (col[t * words] >> (node & 31)) & 1u;
+    const int lo = max(t * G - first, 0), hi = min((t + 1) * G - first, X);  // its rows: [lo, hi)
+    bits |= yes ? rows_from(lo) & ~rows_from(hi) : 0u;
+  }
+  return bits;
+}
+
 // The error bits of node t of batch b.
 __device__ __forceinline__ uint32_t draft_errors(const int32_t* lens, const int32_t* parents, int b, int t, int T, int N) {
   const int n = __ldg(lens + b);

@@ -33,7 +33,7 @@ struct KeyWeightParams {
   int32_t B, Hq, Hkv, G, T, N, R;
   int32_t row0, qtiles;          // rows of this pass: row0 .., in qtiles (1 or 2) tiles of NR
   int32_t ring, words, ctas;     // K units; 32-bit words of a row's nodes; CTAs of the line
-  float scale_log2, decay;
+  float scale_log2, decay, unscale;  // unscale: 1 / scale_log2
   const __nv_bfloat16* q;
   int64_t qs[3];
   const float *lse, *row_scale, *w_in;
@@ -52,7 +52,7 @@ struct Cfg {
   static constexpr int kConst = NR * 128;           // constants of the rows: 32 bytes for each row tile
   // Bytes besides the ring (first) and Q (next): ones, constants, signs, partial sums, who sees what, barriers.
   static constexpr int rest(int qtiles, int T, int words) {
-    return kChunk + kConst + qtiles * NR * 4 + 2 * kSoftThreads * 4 + (words > 0 ? T * 4 + T * words * 4 : 0) + 16 + kBars * 8 + 16;
+    return kChunk + kConst + qtiles * NR * 4 + 2 * kSoftThreads * 4 + 32 + (words > 0 ? T * 4 + T * words * 4 : 0) + 16 + kBars * 8 + 16;
   }
 };
 
@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sConst = sOnes + kChunk;                                    // [NR]
   float* sSign = reinterpret_cast<float*>(sConst + C::kConst);         // [qtiles * NR] of the row's scale; 0: it is left out
   float* sPart = sSign + p.qtiles * NR;                                // [2][kGroups][128]
-  uint64_t* full = reinterpret_cast<uint64_t*>(sPart + 2 * kSoftThreads);  // [ring]
+  uint32_t* sActive = reinterpret_cast<uint32_t*>(sPart + 2 * kSoftThreads);  // [8] bits: the row counts
+  uint64_t* full = reinterpret_cast<uint64_t*>(sActive + 8);           // [ring]
   uint64_t* empty = full + kMaxRing;
   uint64_t* q_full = empty + kMaxRing;
   uint64_t* s_full = q_full + 1;         // [kGroups]
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_full, kSoftThreads);
     mbar_init(drain, 1);
     *s_abort = 0;
+    *s_minus = 0;
     fence_mbarrier_init();
   }
   if (warp == kGroups * 4) {
@@ -212,32 +214,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the pair's rows (all of the last pair's S and sums are done) ----
       // Rows that count for nothing, whatever they hold, become Q = 0 with a constant that
       // no exponential survives.
-      if (threadIdx.x == 0) *s_minus = 0;
-      named_barrier(1, kSoftThreads);
-      for (int i = threadIdx.x; i < p.qtiles * NR; i += kSoftThreads) {
-        const int row = p.row0 + i, r = i % NR, q = i / NR;
+      {
+        const int i = threadIdx.x, row = p.row0 + i, r = i % NR, q = i / NR;
+        const bool real = i < p.qtiles * NR;
         float c = -1e30f, sign = 0.f;
-        if (row < p.R) {
-          const int t = row / p.G, h = w.g * p.G + row % p.G;
+        if (real && row < p.R) {
+          const int t = row / p.G, h = w.g * p.G + row - t * p.G;
           const float lse = __ldg(p.lse + (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t);
           const float scale = p.row_scale ? __ldg(p.row_scale + static_cast<int64_t>(w.b) * p.T + t) : 1.f;
-          if (scale != 0.f && lse != -INFINITY && !(par && __ldg(par + t) == -2)) {
+          const int up = par ? __ldg(par + t) : 0;
+          if (scale != 0.f && lse != -INFINITY && up != -2) {
             sign = scale < 0.f ? -1.f : 1.f;
             if (scale < 0.f) *s_minus = 1;
-            c = (log2f(fabsf(scale)) - lse * 1.4426950408889634f) / p.scale_log2;  // in the scores' unit
+            c = (log2f(fabsf(scale)) - lse * 1.4426950408889634f) * p.unscale;  // in the scores' unit
           }
         }
-        sSign[i] = sign;
-        uint32_t part[3];
+        const unsigned active = __ballot_sync(0xffffffffu, sign != 0.f);
+        if (lane == 0 && real) sActive[warp] = active;
+        if (real) {
+          sSign[i] = sign;
+          uint32_t part[3];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const __nv_bfloat16 y = __float2bfloat16_rn(c);
-          part[k] = __bfloat16_as_ushort(y);
-          c = isfinite(__bfloat162float(y)) ? c - __bfloat162float(y) : 0.f;
+          for (int k = 0; k < 3; ++k) {
+            const __nv_bfloat16 y = __float2bfloat16_rn(c);
+            part[k] = __bfloat16_as_ushort(y);
+            c = isfinite(__bfloat162float(y)) ? c - __bfloat162float(y) : 0.f;
+          }
+          uint8_t* to = sConst + r * 128;
+          *reinterpret_cast<uint4*>(to + (((2 * q) ^ (r & 7)) << 4)) = make_uint4(part[0] | part[1] << 16, part[2], 0u, 0u);
+          *reinterpret_cast<uint4*>(to + (((2 * q + 1) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
         }
-        uint8_t* to = sConst + r * 128;
-        *reinterpret_cast<uint4*>(to + (((2 * q) ^ (r & 7)) << 4)) = make_uint4(part[0] | part[1] << 16, part[2], 0u, 0u);
-        *reinterpret_cast<uint4*>(to + (((2 * q + 1) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
       }
       if (par && w.t1 * kKeys > w.len)
         for (int i = threadIdx.x; i < p.T; i += kSoftThreads) sPar[i] = __ldg(par + i);
@@ -257,15 +263,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         const int u = threadIdx.x % (D / 8);
         const __nv_bfloat16* src = p.q + w.b * p.qs[0] + static_cast<int64_t>(w.g) * p.G * p.qs[1] + u * 8;
-#pragma unroll 4
-        for (int i = threadIdx.x / (D / 8); i < p.qtiles * NR; i += kSoftThreads / (D / 8)) {
-          const int row = p.row0 + i, r = i % NR;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (sSign[i] != 0.f) {
-            const int t = row / p.G, h = row - t * p.G;
-            x = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
+        constexpr int kStep = kSoftThreads / (D / 8), kBatch = NR < kStep ? 1 : NR / kStep < 4 ? NR / kStep : 4;  // rows at a time
+        for (int i0 = threadIdx.x / (D / 8); i0 < p.qtiles * NR; i0 += kBatch * kStep) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int y = 0; y < kBatch; ++y) {
+            const int row = min(p.row0 + i0 + y * kStep, p.R - 1), t = row / p.G, h = row - t * p.G;
+            x[y] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
           }
-          *reinterpret_cast<uint4*>(sQ + (i / NR) * C::kQTile + (u >> 3) * (NR * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x;
+#pragma unroll
+          for (int y = 0; y < kBatch; ++y) {
+            const int i = i0 + y * kStep, r = i % NR;
+            if (i >= p.qtiles * NR) break;
+            if (sSign[i] == 0.f) x[y] = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(sQ + (i / NR) * C::kQTile + (u >> 3) * (NR * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x[y];
+          }
         }
       }
       fence_proxy_async_smem();
@@ -301,23 +313,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           // Negative scales, or drafted keys: a thread leaves out the rows that do not see its own.
-          int tt = (p.row0 + rt * NR) / p.G, hh = (p.row0 + rt * NR) % p.G;
           float sum = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < NR; c += 16) {
-            uint32_t x[16];
-            tmem_ld_32x32b_x16(st + c, x);
+          for (int c = 0; c < NR; c += X) {
+            const int first = p.row0 + rt * NR + c;
+            uint32_t see = (sActive[(rt * NR + c) >> 5] >> (c & 31)) & (X == 32 ? ~0u : (1u << X) - 1u);
+            if (j >= w.len) see = j < end ? see & (par ? rows_seeing<X>(sSeen, p.words, node, first, p.G, p.T) : rows_from(node * p.G - first)) : 0u;
+            uint32_t x[X];
+            if constexpr (X == 16) tmem_ld_32x32b_x16(st + c, x);
+            else tmem_ld_32x32b_x32(st + c, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              bool see = tt < p.T;
-              if (see && j >= w.len) see = j < end && (par ? (sSeen[tt * p.words + (node >> 5)] >> (node & 31)) & 1 : node <= tt);
-              const float sign = sSign[rt * NR + c + i];
-              if (see && sign != 0.f) sum = fmaf(ex2_approx(__uint_as_float(x[i]) * p.scale_log2), sign, sum);
-              if (++hh == p.G) {
-                hh = 0;
-                ++tt;
-              }
+            for (int i = 0; i < X; ++i) {
+              const float e = ex2_approx(__uint_as_float(x[i]) * p.scale_log2);
+              sum = fmaf(see >> i & 1 ? e : 0.f, sSign[rt * NR + c + i], sum);
             }
           }
           acc[0] = f2_pack(sum, 0.f);
@@ -339,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mine) p.w_out[out0 + j] = add ? fmaf(p.decay, old, sum) : sum;
         ++k;
       }
+      if (threadIdx.x == 0) *s_minus = 0;
       named_barrier(1, kSoftThreads);  // every sum of the pair is done
     } while (w.next(ln));
     if (*s_abort && threadIdx.x == 0) atomicOr(p.err, MFA_DEVERR_TIMEOUT);
@@ -408,6 +418,7 @@ extern "C" mfa_status mfa_key_weights(const mfa_tensor* q, const mfa_tensor* k, 
   p.G = static_cast<int32_t>(q->H / k->H); p.T = static_cast<int32_t>(q->N); p.N = static_cast<int32_t>(k->N);
   p.R = p.T * p.G;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(q->D)));
+  p.unscale = static_cast<float>(std::sqrt(static_cast<double>(q->D)) / 1.4426950408889634);
   p.decay = decay;
   p.q = static_cast<const __nv_bfloat16*>(q->data);
   for (int a = 0; a < 3; ++a) p.qs[a] = q->stride[a];

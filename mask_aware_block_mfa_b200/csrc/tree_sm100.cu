@@ -419,25 +419,30 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
               finite = bad == 0;
             }
           }
-          int tt = row0 / p.G, hh = row0 % p.G;
+          uint32_t see = rows >= W ? ~0u : rows > 0 ? (1u << rows) - 1u : 0u;  // rows that see key j, as bits
+          if (j >= w.len) {
+            if (!held) {
+              see = 0u;
+            } else if (par) {
+              uint32_t bits = 0u;
+#pragma unroll 8
+              for (int c = 0; c < W; ++c) bits |= ((sSeen[c * kSeenWords + (node >> 5)] >> (node & 31)) & 1u) << c;
+              see &= bits;
+            } else {
+              see &= rows_from(node * p.G - row0);
+            }
+            if (!finite)
+              for (int c = 0; c < W; ++c)
+                if (see >> c & 1) sPoison[col0 + c] = 1;
+          }
 #pragma unroll 1
           for (int c = 0; c < W; c += 16) {
             uint32_t x[16];
             tmem_ld_32x32b_x16(st + c, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (j >= w.len) {
-                bool see = held && c + i < rows;
-                if (see) see = par ? (sSeen[(c + i) * kSeenWords + (node >> 5)] >> (node & 31)) & 1 : node <= tt;
-                if (!see) x[i] = 0xff800000u;
-                else if (!finite) sPoison[col0 + c + i] = 1;
-              }
-              if (++hh == p.G) {
-                hh = 0;
-                ++tt;
-              }
-            }
+            for (int i = 0; i < 16; ++i)
+              if (j >= w.len && !(see >> (c + i) & 1)) x[i] = 0xff800000u;
             tmem_st_32x32b_x16(st + c, x);
           }
           tmem_st_wait();
