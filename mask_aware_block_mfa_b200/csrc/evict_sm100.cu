@@ -9,13 +9,22 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Selection. The k largest of m weights by radix selection: a weight becomes an
-// unsigned key of the same order, and four passes of eight bits, from the
-// top, narrow down the k-th largest key: each counts the keys that agree with
-// the bits found so far by their next eight bits. Keys above the k-th are
-// kept, and of those equal to it the first ones by index.
+// unsigned key of the same order, and three passes of 11, 11 and 10 bits, from
+// the top, narrow down the k-th largest key: each counts the keys that agree
+// with the bits found so far by their next bits. Keys above the k-th are kept, and
+// of those equal to it the first ones by index.
+//
+// One block per (batch, head). The keys stay in registers (up to 8 per thread) or in
+// shared memory (up to kSelShared), so that the weights are read once; longer
+// lists are read again for each pass (they sit in L2). A warp owns a run of keys, so that the kept rows' places follow
+// from ballots and one scan over the warps. Equal keys would serialise the
+// shared-memory atomics, and accumulated weights hold many zeros: zeros, and
+// the keys that share the first active lane's count, are added per warp.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kSelShared = 52 * 1024;
 
 struct SelectParams {
   const float* weights;
@@ -32,11 +41,17 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   if (x == 0.f) u = 0u;
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+constexpr uint32_t kZeroKey = 0x80000000u;
 
-__global__ void __launch_bounds__(kSelThreads) mfa_select_kernel(const SelectParams p) {
-  __shared__ int hist[256];
+// PER: keys per thread in registers; 0: in shared memory; -1: read again for each pass.
+template <int PER>
+__global__ void __launch_bounds__(kSelThreads) mfa_select_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ int hist[kBins];
+  __shared__ int s_sum[kSelWarps], s_gt[kSelWarps], s_eq[kSelWarps];
   __shared__ int s_bin, s_left;
-  __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
+  extern __shared__ uint32_t s_keys[];
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.x, b = blockIdx.y;
   const int raw = __ldg(p.lens + b);
@@ -57,35 +72,94 @@ __global__ void __launch_bounds__(kSelThreads) mfa_select_kernel(const SelectPar
   for (int t = threadIdx.x; t < p.recent; t += kSelThreads) keep[k + t] = m + t;
   if (k == 0) return;
   const float* w = p.weights + row * p.N;
+  // Warp `warp` owns keys [j0, j1), lane `lane` every 32nd of them.
+  const int seg = (m + kSelThreads - 1) / kSelThreads * 32;
+  const int j0 = min(warp * seg, m), j1 = min(j0 + seg, m);
+  uint32_t reg[PER > 0 ? PER : 1];
+  if constexpr (PER > 0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int j = j0 + i * 32 + lane;
+      reg[i] = j < j1 ? __float_as_uint(__ldg(w + j)) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) reg[i] = order_key(__uint_as_float(reg[i]));
+  } else if constexpr (PER == 0) {
+#pragma unroll 8
+    for (int j = j0 + lane; j < j1; j += 32) s_keys[j] = order_key(__ldg(w + j));
+    __syncwarp();
+  }
+  // Calls f(j, key, valid) for the warp's keys in order, all lanes together.
+  auto each = [&](auto f) {
+    if constexpr (PER > 0) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (j0 + i * 32 >= j1) break;
+        const int j = j0 + i * 32 + lane;
+        f(j, reg[i], j < j1);
+      }
+    } else {
+#pragma unroll 4
+      for (int j = j0 + lane; j - lane < j1; j += 32)
+        f(j, j < j1 ? (PER == 0 ? s_keys[j] : order_key(__ldg(w + j))) : 0u, j < j1);
+    }
+  };
   uint32_t prefix = 0;
   int left = k;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-    for (int j = threadIdx.x; j < m; j += kSelThreads) {
-      const uint32_t key = order_key(__ldg(w + j));
-      if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
+    int zeros = 0;
+    each([&](int, uint32_t key, bool valid) {
+      const bool in = valid && (pass == 0 || (key >> above) == prefix);
+      const bool zero = in && key == kZeroKey;
+      zeros += zero;
+      const unsigned act = __ballot_sync(0xffffffffu, in && !zero);
+      if (act == 0) return;
+      const int bin = (key >> shift) & mask, lead = __ffs(act) - 1;
+      const int first = __shfl_sync(0xffffffffu, bin, lead);  // (all lanes: not behind a condition of the lane's own)
+      const bool same = in && !zero && bin == first;
+      const unsigned run = __ballot_sync(0xffffffffu, same);
+      if (lane == lead) atomicAdd(&hist[bin], __popc(run));
+      else if (in && !zero && !same) atomicAdd(&hist[bin], 1);
+    });
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if (lane == 0 && zeros > 0) atomicAdd(&hist[(kZeroKey >> shift) & mask], zeros);
+    __syncthreads();
+    // The bin that holds the left-th largest: thread t looks at bins top - 2t and top - 2t - 1.
+    const int hi = static_cast<int>(kBins) - 1 - 2 * threadIdx.x;
+    const int a = hist[hi], c = hist[hi - 1];
+    int sum = a + c;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, x);
+      if (lane >= x) sum += o;
+    }
+    if (lane == 31) s_sum[warp] = sum;
+    __syncthreads();
+    int base = lane < warp ? s_sum[lane] : 0;
+    base = __reduce_add_sync(0xffffffffu, base);
+    const int before = base + sum - a - c;  // keys in higher bins
+    if (before < left && before + a >= left) {
+      s_bin = hi;
+      s_left = left - before;
+    } else if (before + a < left && before + a + c >= left) {
+      s_bin = hi - 1;
+      s_left = left - before - a;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      int bin = 255, rest = left;
-      while (hist[bin] < rest) rest -= hist[bin--];
-      s_bin = bin;
-      s_left = rest;
-    }
-    __syncthreads();
-    prefix = (prefix << 8) | static_cast<uint32_t>(s_bin);
+    prefix = (prefix << (pass == 2 ? 10 : 11)) | static_cast<uint32_t>(s_bin);
     left = s_left;
   }
   // prefix is the k-th largest key, `left` of its equals are kept.
-  const int seg = ((m + kSelThreads - 1) / kSelThreads) * 32;
-  const int j0 = warp * seg, j1 = min(m, j0 + seg);
   int gt = 0, eq = 0;
-  for (int j = j0 + lane; j < j1; j += 32) {
-    const uint32_t key = order_key(__ldg(w + j));
-    gt += key > prefix;
-    eq += key == prefix;
-  }
+  each([&](int, uint32_t key, bool valid) {
+    gt += valid && key > prefix;
+    eq += valid && key == prefix;
+  });
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
@@ -93,34 +167,23 @@ __global__ void __launch_bounds__(kSelThreads) mfa_select_kernel(const SelectPar
     s_eq[warp] = eq;
   }
   __syncthreads();
-  gt = eq = 0;
-  for (int x = 0; x < warp; ++x) {
-    gt += s_gt[x];
-    eq += s_eq[x];
-  }
-  for (int base = j0; base < j1; base += 32) {
-    const int j = base + lane;
-    const uint32_t key = j < j1 ? order_key(__ldg(w + j)) : 0u;
-    const bool is_gt = j < j1 && key > prefix, is_eq = j < j1 && key == prefix;
+  gt = __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
+  eq = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
+  each([&](int j, uint32_t key, bool valid) {
+    const bool is_gt = valid && key > prefix, is_eq = valid && key == prefix;
     const unsigned below = (1u << lane) - 1u;
     const unsigned bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
     const int eb = eq + __popc(be & below);
     if (is_gt || (is_eq && eb < left)) keep[gt + __popc(bg & below) + min(eb, left)] = j;
     gt += __popc(bg);
     eq += __popc(be);
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
-// Moving rows together. In place the destination rows are the sources of
-// earlier or the same entries only (idx[t] >= t), so a block that takes the
-// entries in order, a chunk at a time, and loads a whole chunk before it
-// stores any of it, reads every row before it is overwritten. Blocks share
-// nothing: each moves its own slice of a head's columns.
+// Moving rows together. Bound: HBM, every kept row read and written once.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
-constexpr int kSlice = 4;                            // 16-byte units of a row per block
-constexpr int kMoveRows = kMoveThreads / kSlice;     // entries per chunk
 
 struct CompactParams {
   int32_t B, Hkv, idx_heads, n_idx, units;  // units: 16-byte units of a row
@@ -135,58 +198,169 @@ struct CompactParams {
   uint32_t* err;
 };
 
-__global__ void __launch_bounds__(kMoveThreads) mfa_compact_kernel(const CompactParams p) {
-  const int g = blockIdx.y, b = blockIdx.z;
-  const int slices = (p.units + kSlice - 1) / kSlice;
-  const int64_t s = p.start ? __ldg(p.start + b) : 0;
-  const int count = min(max(__ldg(p.count + b), 0), p.n_idx);
-  const int32_t* idx = p.idx + (static_cast<int64_t>(b) * p.idx_heads + (p.idx_heads == 1 ? 0 : g)) * p.n_idx;
+// One (batch, head)'s list.
+struct Moves {
+  int64_t s;
+  int count;
+  const int32_t* idx;
+  __device__ __forceinline__ Moves(const CompactParams& p, int g, int b) {
+    s = p.start ? __ldg(p.start + b) : 0;
+    count = min(max(__ldg(p.count + b), 0), p.n_idx);
+    idx = p.idx + (static_cast<int64_t>(b) * p.idx_heads + (p.idx_heads == 1 ? 0 : g)) * p.n_idx;
+  }
   // The source row of entry t, or -1 when it moves nothing.
-  auto source = [&](int t, bool report) -> int64_t {
+  __device__ __forceinline__ int64_t source(const CompactParams& p, int t, bool report) const {
     const int64_t x = __ldg(idx + t);
     const bool bad = x < 0 || s + x < 0 || s + x >= p.N || s + t < 0 || s + t >= p.N_out || (p.in_place && x < t);
     if (bad && report) atomicOr(p.err, MFA_DEVERR_SEL);
     return bad || (p.in_place && x == t) ? -1 : s + x;
+  }
+};
+
+__device__ __forceinline__ void zero_tail(const CompactParams& p, const Moves& mv, float* dst, int b, int64_t first, int64_t step) {
+  if (!p.zero_end) return;
+  const int64_t z = min(static_cast<int64_t>(__ldg(p.zero_end + b)), p.N_out);
+  for (int64_t j = max(mv.s + mv.count, int64_t(0)) + first; j < z; j += step) dst[j] = 0.f;
+}
+
+// Into other tensors: a block takes kApartRows entries of a list, K and V. UNITS: 16-byte
+// units of a row (0: any number).
+constexpr int kApartRows = 64;
+template <int UNITS>
+__global__ void __launch_bounds__(kMoveThreads) mfa_compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ int64_t s_row[kApartRows];
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = blockIdx.y, b = blockIdx.z, units = UNITS > 0 ? UNITS : p.units;
+  const Moves mv(p, g, b);
+  const int base = blockIdx.x * kApartRows;
+  float* w_out = p.w_out ? p.w_out + (static_cast<int64_t>(b) * p.Hkv + g) * p.N_out : nullptr;
+  if (w_out) zero_tail(p, mv, w_out, b, blockIdx.x * kMoveThreads + threadIdx.x, static_cast<int64_t>(gridDim.x) * kMoveThreads);
+  if (base >= mv.count) return;
+  if (threadIdx.x < kApartRows) {
+    const int t = base + threadIdx.x;
+    const int64_t r = t < mv.count ? mv.source(p, t, true) : -1;
+    s_row[threadIdx.x] = r;
+    if (w_out && r >= 0) w_out[mv.s + t] = p.w[(static_cast<int64_t>(b) * p.Hkv + g) * p.N + r];
+  }
+  __syncthreads();
+  const uint4* ks = p.k + b * p.ks[0] + g * p.ks[1];
+  const uint4* vs = p.v + b * p.vs[0] + g * p.vs[1];
+  uint4* ko = p.k_out + b * p.kos[0] + g * p.kos[1] + (mv.s + base) * p.kos[2];
+  uint4* vo = p.v_out + b * p.vos[0] + g * p.vos[1] + (mv.s + base) * p.vos[2];
+  constexpr int kBatch = 4;
+  for (int i0 = threadIdx.x; i0 < kApartRows * units; i0 += kBatch * kMoveThreads) {
+    uint4 x[kBatch], y[kBatch];
+    int64_t r[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = i0 + i * kMoveThreads, t = e / units, u = e - t * units;
+      r[i] = e < kApartRows * units ? s_row[t] : -1;
+      if (r[i] >= 0) {
+        x[i] = ks[r[i] * p.ks[2] + u];
+        y[i] = vs[r[i] * p.vs[2] + u];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = i0 + i * kMoveThreads, t = e / units, u = e - t * units;
+      if (r[i] >= 0) {
+        ko[t * p.kos[2] + u] = x[i];
+        vo[t * p.vos[2] + u] = y[i];
+      }
+    }
+  }
+}
+
+// In place. The destinations are the sources of earlier or the same entries
+// only (idx[t] >= t), so a block that takes the entries in order, a chunk at a
+// time, and loads a whole chunk before it stores any of it, reads every row
+// before it is overwritten; the next chunk's rows lie behind all that this
+// one writes, so they may be loaded before. Blocks share nothing: each moves its own
+// slice of the columns of one head's K or V, one more block the weights.
+constexpr int kSlice = 4;   // 16-byte units of a row per block
+constexpr int kBatch = 4;   // entries per thread and chunk
+
+// Entries first .. of a block's list through load(t) and store(t, x), as described.
+template <typename T, typename Load, typename Store>
+__device__ __forceinline__ void move_in_order(int count, int first, int step, Load load, Store store) {
+  T x[2][kBatch];
+  bool have[2][kBatch];
+  auto fetch = [&](int base, T (&v)[kBatch], bool (&h)[kBatch]) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = base + first + i * step;
+      h[i] = t < count && load(t, v[i]);
+    }
   };
+  auto put = [&](int base, const T (&v)[kBatch], const bool (&h)[kBatch]) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (h[i]) store(base + first + i * step, v[i]);
+  };
+  const int chunk = kBatch * step;
+  fetch(0, x[0], have[0]);
+  for (int base = 0; base < count; base += 2 * chunk) {
+    __syncthreads();
+    fetch(base + chunk, x[1], have[1]);
+    put(base, x[0], have[0]);
+    __syncthreads();
+    fetch(base + 2 * chunk, x[0], have[0]);
+    put(base + chunk, x[1], have[1]);
+  }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) mfa_compact_in_place_kernel(const __grid_constant__ CompactParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = blockIdx.y, b = blockIdx.z;
+  const int slices = (p.units + kSlice - 1) / kSlice;
+  const Moves mv(p, g, b);
   if (blockIdx.x < 2 * slices) {
     const bool isv = blockIdx.x >= slices;
     const int slice = blockIdx.x - (isv ? slices : 0);
     const int u = slice * kSlice + threadIdx.x % kSlice;
-    const int64_t* si = isv ? p.vs : p.ks;
-    const int64_t* so = isv ? p.vos : p.kos;
-    const uint4* src = (isv ? p.v : p.k) + b * si[0] + g * si[1] + u;
-    uint4* dst = (isv ? p.v_out : p.k_out) + b * so[0] + g * so[1] + u;
-    for (int base = 0; base < count; base += kMoveRows) {
-      const int t = base + threadIdx.x / kSlice;
-      int64_t r = -1;
-      uint4 x;
-      if (t < count && u < p.units) {
-        r = source(t, blockIdx.x == 0);
-        if (r >= 0) x = src[r * si[2]];
-      }
-      __syncthreads();
-      if (r >= 0) dst[(s + t) * so[2]] = x;
-    }
-  } else if (p.w_out) {
-    const float* src = p.w + (static_cast<int64_t>(b) * p.Hkv + g) * p.N;
-    float* dst = p.w_out + (static_cast<int64_t>(b) * p.Hkv + g) * p.N_out;
-    for (int base = 0; base < count; base += kMoveThreads) {
-      const int t = base + threadIdx.x;
-      int64_t r = -1;
-      float x = 0.f;
-      if (t < count) {
-        r = source(t, false);
-        if (r >= 0) x = src[r];
-      }
-      __syncthreads();
-      if (r >= 0) dst[s + t] = x;
-    }
+    const int64_t step = isv ? p.vs[2] : p.ks[2];
+    uint4* at = isv ? p.v_out + b * p.vs[0] + g * p.vs[1] + u : p.k_out + b * p.ks[0] + g * p.ks[1] + u;
+    move_in_order<uint4>(
+        mv.count, threadIdx.x / kSlice, kMoveThreads / kSlice,
+        [&](int t, uint4& x) {
+          if (u >= p.units) return false;
+          const int64_t r = mv.source(p, t, blockIdx.x == 0);
+          if (r >= 0) x = at[r * step];
+          return r >= 0;
+        },
+        [&](int t, const uint4& x) { at[(mv.s + t) * step] = x; });
+  } else {
+    float* at = p.w_out + (static_cast<int64_t>(b) * p.Hkv + g) * p.N;
+    move_in_order<float>(
+        mv.count, threadIdx.x, kMoveThreads,
+        [&](int t, float& x) {
+          const int64_t r = mv.source(p, t, false);
+          if (r >= 0) x = at[r];
+          return r >= 0;
+        },
+        [&](int t, float x) { at[mv.s + t] = x; });
     __syncthreads();
-    if (p.zero_end) {
-      const int64_t z = min(static_cast<int64_t>(__ldg(p.zero_end + b)), p.N_out);
-      for (int64_t j = max(s + count, int64_t(0)) + threadIdx.x; j < z; j += kMoveThreads) dst[j] = 0.f;
-    }
+    zero_tail(p, mv, at, b, threadIdx.x, kMoveThreads);
   }
+}
+
+// A launch that may begin while the kernel before it in the stream ends (it waits for that
+// kernel before it reads anything).
+template <typename P>
+bool launch_after(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
 }
 
 // The bytes of a [B, H, N, ...] tensor, first to last, as an address range.
@@ -218,8 +392,19 @@ extern "C" mfa_status mfa_evict_select(const float* weights, const int32_t* lens
   if (N >= (1 << 30) || budget >= (1 << 30) || Hkv > 65535 || B > 65535 || static_cast<int64_t>(B) * Hkv > (1 << 24))
     return MFA_ERR_UNSUPPORTED;
   SelectParams p{weights, lens, Hkv, N, budget, recent, keep, new_lens, dev_err};
-  mfa_select_kernel<<<dim3(Hkv, B), kSelThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MFA_OK : MFA_ERR_CUDA;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const dim3 grid(Hkv, B);
+  bool ok;
+  if (N <= 2 * kSelThreads) ok = launch_after(mfa_select_kernel<2>, grid, kSelThreads, 0, cs, p);
+  else if (N <= 8 * kSelThreads) ok = launch_after(mfa_select_kernel<8>, grid, kSelThreads, 0, cs, p);
+  else if (N <= kSelShared) {
+    static std::atomic<uint64_t> attr_devs{0};
+    if (!ensure_smem_attr(reinterpret_cast<const void*>(mfa_select_kernel<0>), kSelShared * 4, attr_devs)) return MFA_ERR_CUDA;
+    ok = launch_after(mfa_select_kernel<0>, grid, kSelThreads, static_cast<size_t>(N) * 4, cs, p);
+  } else {
+    ok = launch_after(mfa_select_kernel<-1>, grid, kSelThreads, 0, cs, p);
+  }
+  return ok ? MFA_OK : MFA_ERR_CUDA;
 }
 
 extern "C" mfa_status mfa_cache_compact(const mfa_tensor* k, const mfa_tensor* v, const float* weights,
@@ -270,8 +455,14 @@ extern "C" mfa_status mfa_cache_compact(const mfa_tensor* k, const mfa_tensor* v
   }
   p.w = weights; p.w_out = weights_out;
   p.start = start; p.idx = idx; p.count = count; p.zero_end = zero_end; p.err = dev_err;
-  const int slices = (p.units + kSlice - 1) / kSlice;
-  const dim3 grid(2 * slices + (weights ? 1 : 0), p.Hkv, p.B);
-  mfa_compact_kernel<<<grid, kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MFA_OK : MFA_ERR_CUDA;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (in_place) {
+    const int slices = (p.units + kSlice - 1) / kSlice;
+    const dim3 grid(2 * slices + (weights ? 1 : 0), p.Hkv, p.B);
+    return launch_after(mfa_compact_in_place_kernel, grid, kMoveThreads, 0, cs, p) ? MFA_OK : MFA_ERR_CUDA;
+  }
+  const dim3 grid(static_cast<unsigned>(n_idx > 0 ? cdiv64(n_idx, kApartRows) : 1), p.Hkv, p.B);
+  auto* kernel = p.units == 8 ? mfa_compact_kernel<8> : p.units == 16 ? mfa_compact_kernel<16>
+               : p.units == 32 ? mfa_compact_kernel<32> : mfa_compact_kernel<0>;
+  return launch_after(kernel, grid, kMoveThreads, 0, cs, p) ? MFA_OK : MFA_ERR_CUDA;
 }
