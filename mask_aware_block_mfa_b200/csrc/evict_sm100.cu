@@ -14,17 +14,21 @@ namespace {
 // with the bits found so far by their next bits. Keys above the k-th are kept, and
 // of those equal to it the first ones by index.
 //
-// One block per (batch, head). The keys stay in registers (up to 8 per thread) or in
-// shared memory (up to kSelShared), so that the weights are read once; longer
-// lists are read again for each pass (they sit in L2). A warp owns a run of keys, so that the kept rows' places follow
-// from ballots and one scan over the warps. Equal keys would serialise the
-// shared-memory atomics, and accumulated weights hold many zeros: zeros, and
-// the keys that share the first active lane's count, are added per warp.
+// One block per (batch, head) holds its keys in shared memory, so that the
+// weights are read once (lists beyond kSelShared keys are read again for each
+// pass; they sit in L2). A warp owns a run of keys, so that the kept rows'
+// places follow from ballots and one scan over the warps. Bound: issue slots and
+// the counters' atomics. Equal keys serialise those, and accumulated weights
+// hold many zeros: zeros are counted in a register, and 32 keys of one bin
+// by one lane. (A cluster of 2 to 8 blocks per list, each counting its share and
+// reading the others' counts, measured 20 us against 12 on 15 lists of 20011: its
+// three barriers and remote reads cost more than the shorter passes save.)
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kSelShared = 52 * 1024;
+constexpr int kRun = 128;               // a warp's keys at a time, four per lane
+constexpr int kSelShared = 48 * 1024;   // with hist, what a block may hold
 
 struct SelectParams {
   const float* weights;
@@ -43,13 +47,14 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 constexpr uint32_t kZeroKey = 0x80000000u;
 
-// PER: keys per thread in registers; 0: in shared memory; -1: read again for each pass.
-template <int PER>
-__global__ void __launch_bounds__(kSelThreads) mfa_select_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ int hist[kBins];
+// SHARED: the keys in shared memory; otherwise read again for each pass.
+template <bool SHARED>
+__global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ int hist[3][kBins];
   __shared__ int s_sum[kSelWarps], s_gt[kSelWarps], s_eq[kSelWarps];
   __shared__ int s_bin, s_left;
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];
+  for (int i = threadIdx.x; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -72,66 +77,58 @@ __global__ void __launch_bounds__(kSelThreads) mfa_select_kernel(const __grid_co
   for (int t = threadIdx.x; t < p.recent; t += kSelThreads) keep[k + t] = m + t;
   if (k == 0) return;
   const float* w = p.weights + row * p.N;
-  // Warp `warp` owns keys [j0, j1), lane `lane` every 32nd of them.
-  const int seg = (m + kSelThreads - 1) / kSelThreads * 32;
-  const int j0 = min(warp * seg, m), j1 = min(j0 + seg, m);
-  uint32_t reg[PER > 0 ? PER : 1];
-  if constexpr (PER > 0) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int j = j0 + i * 32 + lane;
-      reg[i] = j < j1 ? __float_as_uint(__ldg(w + j)) : 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) reg[i] = order_key(__uint_as_float(reg[i]));
-  } else if constexpr (PER == 0) {
+  // A warp owns `seg` keys from j0 on; places past the list hold key 0, which no weight has.
+  const int seg = (m + kSelWarps * kRun - 1) / (kSelWarps * kRun) * kRun, j0 = warp * seg;
+  uint32_t* own = s_keys + j0;
+  if constexpr (SHARED) {
 #pragma unroll 8
-    for (int j = j0 + lane; j < j1; j += 32) s_keys[j] = order_key(__ldg(w + j));
-    __syncwarp();
+    for (int i = lane; i < seg; i += 32) own[i] = j0 + i < m ? order_key(__ldg(w + j0 + i)) : 0u;
   }
-  // Calls f(j, key, valid) for the warp's keys in order, all lanes together.
+  __syncthreads();
+  // Calls f(key) for the warp's keys, all lanes together, in any order.
   auto each = [&](auto f) {
-    if constexpr (PER > 0) {
+#pragma unroll 2
+    for (int i = 0; i < seg; i += kRun) {
+      uint32_t key[4];
+      if constexpr (SHARED) {
+        const uint4 x = *reinterpret_cast<const uint4*>(own + i + lane * 4);
+        key[0] = x.x; key[1] = x.y; key[2] = x.z; key[3] = x.w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if (j0 + i * 32 >= j1) break;
-        const int j = j0 + i * 32 + lane;
-        f(j, reg[i], j < j1);
+        for (int y = 0; y < 4; ++y) {
+          const int j = j0 + i + y * 32 + lane;
+          key[y] = j < m ? order_key(__ldg(w + j)) : 0u;
+        }
       }
-    } else {
-#pragma unroll 4
-      for (int j = j0 + lane; j - lane < j1; j += 32)
-        f(j, j < j1 ? (PER == 0 ? s_keys[j] : order_key(__ldg(w + j))) : 0u, j < j1);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) f(key[y]);
     }
   };
   uint32_t prefix = 0;
   int left = k;
-#pragma unroll 1
+#pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 31 : pass == 1 ? 21 : 10;
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
     int zeros = 0;
-    each([&](int, uint32_t key, bool valid) {
-      const bool in = valid && (pass == 0 || (key >> above) == prefix);
-      const bool zero = in && key == kZeroKey;
-      zeros += zero;
-      const unsigned act = __ballot_sync(0xffffffffu, in && !zero);
-      if (act == 0) return;
-      const int bin = (key >> shift) & mask, lead = __ffs(act) - 1;
-      const int first = __shfl_sync(0xffffffffu, bin, lead);  // (all lanes: not behind a condition of the lane's own)
-      const bool same = in && !zero && bin == first;
-      const unsigned run = __ballot_sync(0xffffffffu, same);
-      if (lane == lead) atomicAdd(&hist[bin], __popc(run));
-      else if (in && !zero && !same) atomicAdd(&hist[bin], 1);
+    each([&](uint32_t key) {
+      const bool in = pass == 0 ? key != 0u : (key >> above) == prefix;
+      const int bin = (key >> shift) & mask;
+      int one = 0;
+      __match_all_sync(0xffffffffu, in && key != kZeroKey ? bin : -1 - lane, &one);
+      if (one) {
+        if (lane == 0) atomicAdd(&hist[pass][bin], 32);
+      } else if (in) {
+        if (key == kZeroKey) ++zeros;
+        else atomicAdd(&hist[pass][bin], 1);
+      }
     });
     zeros = __reduce_add_sync(0xffffffffu, zeros);
-    if (lane == 0 && zeros > 0) atomicAdd(&hist[(kZeroKey >> shift) & mask], zeros);
+    if (lane == 0 && zeros > 0) atomicAdd(&hist[pass][(kZeroKey >> shift) & mask], zeros);
     __syncthreads();
     // The bin that holds the left-th largest: thread t looks at bins top - 2t and top - 2t - 1.
     const int hi = static_cast<int>(kBins) - 1 - 2 * threadIdx.x;
-    const int a = hist[hi], c = hist[hi - 1];
+    const int a = hist[pass][hi], c = hist[pass][hi - 1];
     int sum = a + c;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -156,9 +153,9 @@ __global__ void __launch_bounds__(kSelThreads) mfa_select_kernel(const __grid_co
   }
   // prefix is the k-th largest key, `left` of its equals are kept.
   int gt = 0, eq = 0;
-  each([&](int, uint32_t key, bool valid) {
-    gt += valid && key > prefix;
-    eq += valid && key == prefix;
+  each([&](uint32_t key) {
+    gt += key > prefix;
+    eq += key == prefix;
   });
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
@@ -167,17 +164,21 @@ __global__ void __launch_bounds__(kSelThreads) mfa_select_kernel(const __grid_co
     s_eq[warp] = eq;
   }
   __syncthreads();
+  if (gt + eq == 0) return;  // (of this warp)
   gt = __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
   eq = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
-  each([&](int j, uint32_t key, bool valid) {
-    const bool is_gt = valid && key > prefix, is_eq = valid && key == prefix;
+#pragma unroll 4
+  for (int i = 0; i < seg; i += 32) {
+    const int j = j0 + i + lane;
+    const uint32_t key = SHARED ? own[i + lane] : j < m ? order_key(__ldg(w + j)) : 0u;
+    const bool is_gt = key > prefix, is_eq = key == prefix;
     const unsigned below = (1u << lane) - 1u;
     const unsigned bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
     const int eb = eq + __popc(be & below);
     if (is_gt || (is_eq && eb < left)) keep[gt + __popc(bg & below) + min(eb, left)] = j;
     gt += __popc(bg);
     eq += __popc(be);
-  });
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -393,16 +394,15 @@ extern "C" mfa_status mfa_evict_select(const float* weights, const int32_t* lens
     return MFA_ERR_UNSUPPORTED;
   SelectParams p{weights, lens, Hkv, N, budget, recent, keep, new_lens, dev_err};
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int64_t keys = cdiv64(N, kSelWarps * kRun) * kSelWarps * kRun;  // with every warp's run full
   const dim3 grid(Hkv, B);
   bool ok;
-  if (N <= 2 * kSelThreads) ok = launch_after(mfa_select_kernel<2>, grid, kSelThreads, 0, cs, p);
-  else if (N <= 8 * kSelThreads) ok = launch_after(mfa_select_kernel<8>, grid, kSelThreads, 0, cs, p);
-  else if (N <= kSelShared) {
+  if (keys <= kSelShared) {
     static std::atomic<uint64_t> attr_devs{0};
-    if (!ensure_smem_attr(reinterpret_cast<const void*>(mfa_select_kernel<0>), kSelShared * 4, attr_devs)) return MFA_ERR_CUDA;
-    ok = launch_after(mfa_select_kernel<0>, grid, kSelThreads, static_cast<size_t>(N) * 4, cs, p);
+    if (!ensure_smem_attr(reinterpret_cast<const void*>(mfa_select_kernel<true>), kSelShared * 4, attr_devs)) return MFA_ERR_CUDA;
+    ok = launch_after(mfa_select_kernel<true>, grid, kSelThreads, static_cast<size_t>(keys) * 4, cs, p);
   } else {
-    ok = launch_after(mfa_select_kernel<-1>, grid, kSelThreads, 0, cs, p);
+    ok = launch_after(mfa_select_kernel<false>, grid, kSelThreads, 0, cs, p);
   }
   return ok ? MFA_OK : MFA_ERR_CUDA;
 }
