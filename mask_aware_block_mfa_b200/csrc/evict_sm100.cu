@@ -81,27 +81,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
   const int seg = (m + kSelWarps * kRun - 1) / (kSelWarps * kRun) * kRun, j0 = warp * seg;
   uint32_t* own = s_keys + j0;
   if constexpr (SHARED) {
-#pragma unroll 8
+#pragma unroll 16
     for (int i = lane; i < seg; i += 32) own[i] = j0 + i < m ? order_key(__ldg(w + j0 + i)) : 0u;
   }
   __syncthreads();
-  // Calls f(key) for the warp's keys, all lanes together, in any order.
-  auto each = [&](auto f) {
-#pragma unroll 2
-    for (int i = 0; i < seg; i += kRun) {
-      uint32_t key[4];
-      if constexpr (SHARED) {
-        const uint4 x = *reinterpret_cast<const uint4*>(own + i + lane * 4);
-        key[0] = x.x; key[1] = x.y; key[2] = x.z; key[3] = x.w;
-      } else {
+  // Lane `lane`'s keys j0 + i + 4 * lane .. + 3.
+  auto four = [&](int i, uint32_t (&key)[4]) {
+    if constexpr (SHARED) {
+      const uint4 x = *reinterpret_cast<const uint4*>(own + i + lane * 4);
+      key[0] = x.x; key[1] = x.y; key[2] = x.z; key[3] = x.w;
+    } else {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int j = j0 + i + y * 32 + lane;
-          key[y] = j < m ? order_key(__ldg(w + j)) : 0u;
-        }
+      for (int y = 0; y < 4; ++y) {
+        const int j = j0 + i + lane * 4 + y;
+        key[y] = j < m ? order_key(__ldg(w + j)) : 0u;
       }
-#pragma unroll
-      for (int y = 0; y < 4; ++y) f(key[y]);
     }
   };
   uint32_t prefix = 0;
@@ -111,18 +105,32 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 31 : pass == 1 ? 21 : 10;
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
     int zeros = 0;
-    each([&](uint32_t key) {
-      const bool in = pass == 0 ? key != 0u : (key >> above) == prefix;
-      const int bin = (key >> shift) & mask;
-      int one = 0;
-      __match_all_sync(0xffffffffu, in && key != kZeroKey ? bin : -1 - lane, &one);
-      if (one) {
-        if (lane == 0) atomicAdd(&hist[pass][bin], 32);
-      } else if (in) {
-        if (key == kZeroKey) ++zeros;
-        else atomicAdd(&hist[pass][bin], 1);
+#pragma unroll 2
+    for (int i = 0; i < seg; i += kRun) {
+      uint32_t key[4];
+      four(i, key);
+      bool in[4], any = false;
+      int bin[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        in[y] = pass == 0 ? key[y] != 0u : (key[y] >> above) == prefix;
+        bin[y] = (key[y] >> shift) & mask;
+        any |= in[y];
       }
-    });
+      if (pass > 0 && !__any_sync(0xffffffffu, any)) continue;  // few keys get past the first digit
+      const int first = __shfl_sync(0xffffffffu, bin[0], 0);
+      const bool same = in[0] && in[1] && in[2] && in[3] && bin[0] == first && bin[1] == first && bin[2] == first && bin[3] == first;
+      if (__all_sync(0xffffffffu, same)) {
+        if (lane == 0) atomicAdd(&hist[pass][first], kRun);
+        continue;
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if (!in[y]) continue;
+        if (key[y] == kZeroKey) ++zeros;
+        else atomicAdd(&hist[pass][bin[y]], 1);
+      }
+    }
     zeros = __reduce_add_sync(0xffffffffu, zeros);
     if (lane == 0 && zeros > 0) atomicAdd(&hist[pass][(kZeroKey >> shift) & mask], zeros);
     __syncthreads();
@@ -153,10 +161,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
   }
   // prefix is the k-th largest key, `left` of its equals are kept.
   int gt = 0, eq = 0;
-  each([&](uint32_t key) {
-    gt += key > prefix;
-    eq += key == prefix;
-  });
+#pragma unroll 4
+  for (int i = 0; i < seg; i += kRun) {
+    uint32_t key[4];
+    four(i, key);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      gt += key[y] > prefix;
+      eq += key[y] == prefix;
+    }
+  }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
@@ -167,17 +181,37 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
   if (gt + eq == 0) return;  // (of this warp)
   gt = __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
   eq = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
-#pragma unroll 4
-  for (int i = 0; i < seg; i += 32) {
-    const int j = j0 + i + lane;
-    const uint32_t key = SHARED ? own[i + lane] : j < m ? order_key(__ldg(w + j)) : 0u;
-    const bool is_gt = key > prefix, is_eq = key == prefix;
-    const unsigned below = (1u << lane) - 1u;
-    const unsigned bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-    const int eb = eq + __popc(be & below);
-    if (is_gt || (is_eq && eb < left)) keep[gt + __popc(bg & below) + min(eb, left)] = j;
-    gt += __popc(bg);
-    eq += __popc(be);
+  // A kept key's place: the keys above the k-th before it, and the equal ones that are kept.
+  const unsigned below = (1u << lane) - 1u;
+#pragma unroll 2
+  for (int i = 0; i < seg; i += kRun) {
+    uint32_t key[4];
+    four(i, key);
+    int at = gt, ties = eq;
+    bool tie = false;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const unsigned bg = __ballot_sync(0xffffffffu, key[y] > prefix);
+      at += __popc(bg & below);
+      gt += __popc(bg);
+      tie |= key[y] == prefix;
+    }
+    if (__any_sync(0xffffffffu, tie)) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const unsigned be = __ballot_sync(0xffffffffu, key[y] == prefix);
+        ties += __popc(be & below);
+        eq += __popc(be);
+      }
+    }
+    const int j = j0 + i + lane * 4;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const bool is_gt = key[y] > prefix, is_eq = key[y] == prefix;
+      if (is_gt || (is_eq && ties < left)) keep[at + min(ties, left)] = j + y;
+      at += is_gt;
+      ties += is_eq;
+    }
   }
 }
 
