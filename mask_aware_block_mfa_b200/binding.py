@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -442,16 +443,38 @@ class Decode:
         return 0 if self.err is None else int(self.err.item())
 
 
-def _cache_desc(name: str, t, device, shape=None) -> MfaTensor:
-    """The C descriptor of a bf16 [B, H, N, D] tensor on `device` (the short way:
-    these calls take a few microseconds on the device)."""
+# The calls below take a few microseconds on the device, so their marshalling is
+# kept short: descriptors are packed as bytes and handed over as addresses.
+_DESC = struct.Struct("Pii8q")
+_DESC_BF16 = MFA_BF16
+_cache_lib = None
+
+
+def _cache_fns():
+    """The cache operators' entry points, with descriptors as plain addresses."""
+    global _cache_lib
+    if _cache_lib is None:
+        lib = ctypes.CDLL(load()._name)
+        P, I = ctypes.c_void_p, ctypes.c_int32
+        for name, args in (("mfa_tree_decode", [P] * 8 + [ctypes.c_size_t, P, P]),
+                           ("mfa_key_weights", [P] * 7 + [ctypes.c_float, P, P, P]),
+                           ("mfa_evict_select", [P, P] + [I] * 5 + [P] * 4),
+                           ("mfa_cache_compact", [P] * 5 + [I, I] + [P] * 7)):
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = ctypes.c_int, args
+        _cache_lib = lib
+    return _cache_lib
+
+
+def _cache_desc(name: str, t, device, shape=None) -> bytes:
+    """The C descriptor of a bf16 [B, H, N, D] tensor on `device`."""
     if not isinstance(t, torch.Tensor) or t.device != device:
         _on_device(name, t, device)
     if t.dtype is not torch.bfloat16 or t.dim() != 4:
         raise ValueError(f"{name} must be a bfloat16 tensor of four dimensions, got {t.dtype} {tuple(t.shape)}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return MfaTensor(t.data_ptr(), MFA_BF16, 0, *t.shape, t.stride())
+    return _DESC.pack(t.data_ptr(), _DESC_BF16, 0, *t.shape, *t.stride())
 
 
 def _array_ptr(name: str, t, device, dtype, shape) -> int:
@@ -495,16 +518,15 @@ class _CacheOp:
 
     def _call(self, name: str, fn, *args, stream=None):
         """Call an entry point on `stream` with the object's device current."""
-        if stream is not None:
-            _stream_ptr(stream, self.device)
+        index = self.device.index
+        if stream is None:
+            ptr = torch._C._cuda_getCurrentRawStream(index)
         else:
-            stream = torch.cuda.current_stream(self.device)
-        ptr = stream.cuda_stream
+            ptr = _stream_ptr(stream, self.device)
         for t, home in self._kept:
             if ptr != home:
-                t.record_stream(stream)
-        index = self.device.index
-        if torch.cuda.current_device() == index:
+                t.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+        if torch._C._cuda_getDevice() == index:
             code = fn(*args, ptr)
         else:
             with torch.cuda.device(index):
@@ -524,7 +546,7 @@ class TreeDecode(_CacheOp):
 
     def __init__(self, device="cuda"):
         super().__init__(device)
-        self.ws = None
+        self.ws, self._ws, self._ws_bytes = None, None, 0
         self._need = {}
 
     def __call__(self, q, k, v, lens, parents=None, out=None, lse=None, stream=None):
@@ -545,11 +567,12 @@ class TreeDecode(_CacheOp):
             if need == 0:
                 raise ValueError("invalid tree decode sizes")
             self._need[key] = need
-        if self.ws is None or self.ws.numel() < need or out is None or lse is None:
+        if out is None or lse is None or self._ws_bytes < need:
             with self._on_stream(stream):
-                if self.ws is None or self.ws.numel() < need:
+                if self._ws_bytes < need:
                     # A smaller one stays: a graph captured with it may be replayed.
                     self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
+                    self._ws, self._ws_bytes = self.ws.data_ptr(), need
                     self._kept.append((self.ws, torch.cuda.current_stream(dev).cuda_stream))
                 if out is None:
                     out = torch.empty(q.shape, dtype=q.dtype, device=dev)
@@ -557,8 +580,8 @@ class TreeDecode(_CacheOp):
                     lse = torch.empty(B_, Hq, T, dtype=torch.float32, device=dev)
         od = _cache_desc("out", out, dev, q.shape)
         lse_p = _array_ptr("lse", lse, dev, torch.float32, (B_, Hq, T))
-        self._call("mfa_tree_decode", load().mfa_tree_decode, qd, kd, vd, lens_p, par_p, od, lse_p, self.ws.data_ptr(),
-                   self.ws.numel(), self._err, stream=stream)
+        self._call("mfa_tree_decode", _cache_fns().mfa_tree_decode, qd, kd, vd, lens_p, par_p, od, lse_p, self._ws,
+                   self._ws_bytes, self._err, stream=stream)
         return out, lse
 
 
@@ -584,7 +607,7 @@ class KeyWeights(_CacheOp):
             with self._on_stream(stream):
                 weights_out = torch.zeros(shape, dtype=torch.float32, device=dev)
         out_p = _array_ptr("weights_out", weights_out, dev, torch.float32, shape)
-        self._call("mfa_key_weights", load().mfa_key_weights, qd, kd, lse_p, lens_p, par_p, row_p, in_p, float(decay),
+        self._call("mfa_key_weights", _cache_fns().mfa_key_weights, qd, kd, lse_p, lens_p, par_p, row_p, in_p, float(decay),
                    out_p, self._err, stream=stream)
         return weights_out
 
@@ -620,7 +643,7 @@ class CacheCompact(_CacheOp):
         zero_p = None if zero_end is None else _array_ptr("zero_end", zero_end, dev, torch.int32, (B_,))
         w_p = None if weights is None else _array_ptr("weights", weights, dev, torch.float32, (B_, H, N))
         wo_p = None if weights is None else _array_ptr("weights_out", weights_out, dev, torch.float32, (B_, H, N_out))
-        self._call("mfa_cache_compact", load().mfa_cache_compact, kd, vd, w_p, start_p, idx_p, idx.shape[1],
+        self._call("mfa_cache_compact", _cache_fns().mfa_cache_compact, kd, vd, w_p, start_p, idx_p, idx.shape[1],
                    idx.shape[2], count_p, zero_p, kod, vod, wo_p, self._err, stream=stream)
 
 
@@ -635,6 +658,13 @@ class Evictor(_CacheOp):
         self.compact = CacheCompact(device)
         self.compact.err, self.compact._err, self.compact._kept = self.err, self._err, self._kept
 
+    def _lists(self, B_, H, keep, new_lens):
+        if keep is None:
+            keep = torch.empty(B_, H, self.budget, dtype=torch.int32, device=self.device)
+        if new_lens is None:
+            new_lens = torch.empty(B_, dtype=torch.int32, device=self.device)
+        return keep, new_lens
+
     def select(self, weights, lens, keep=None, new_lens=None, stream=None):
         """keep int32 [B, Hkv, budget] (ascending rows, then -1) and new_lens int32 [B]."""
         dev = self.device
@@ -644,14 +674,14 @@ class Evictor(_CacheOp):
         w_p = _array_ptr("weights", weights, dev, torch.float32, (B_, H, N))
         lens_p = _array_ptr("lens", lens, dev, torch.int32, (B_,))
         if keep is None or new_lens is None:
-            with self._on_stream(stream):
-                if keep is None:
-                    keep = torch.empty(B_, H, self.budget, dtype=torch.int32, device=dev)
-                if new_lens is None:
-                    new_lens = torch.empty(B_, dtype=torch.int32, device=dev)
+            if stream is None:
+                keep, new_lens = self._lists(B_, H, keep, new_lens)
+            else:
+                with torch.cuda.stream(stream):
+                    keep, new_lens = self._lists(B_, H, keep, new_lens)
         keep_p = _array_ptr("keep", keep, dev, torch.int32, (B_, H, self.budget))
         new_p = _array_ptr("new_lens", new_lens, dev, torch.int32, (B_,))
-        self._call("mfa_evict_select", load().mfa_evict_select, w_p, lens_p, B_, H, N, self.budget, self.recent,
+        self._call("mfa_evict_select", _cache_fns().mfa_evict_select, w_p, lens_p, B_, H, N, self.budget, self.recent,
                    keep_p, new_p, self._err, stream=stream)
         return keep, new_lens
 
