@@ -64,7 +64,10 @@ struct Cfg {
   static constexpr int kCols = NR < 32 ? NR : 32;       // rows (registers) per softmax thread
   static constexpr int kGroups = NR / kCols;            // groups of 4 softmax warps
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kThreads = (kSoftWarps + 3) * 32;
+  // With 16 softmax warps the SM's registers come to 96 per thread, of which the
+  // other warps (a fourth one is idle) give some up: 640 x 96 = 512 x 104 + 128 x 64.
+  static constexpr bool kSplitRegs = kSoftWarps == 16;
+  static constexpr int kThreads = (kSoftWarps + (kSplitRegs ? 4 : 3)) * 32;
   static constexpr int kUnits = D == 256 ? 2 : 1;       // ring units of a K (or V) tile
   static constexpr int kUnit = (D == 64 ? 1 : 2) * kChunk;
   static constexpr int kPBytes = (NR + 63) / 64 * kChunk;
@@ -78,7 +81,7 @@ struct Cfg {
   static constexpr int kRing0 = (kQBytes + 1023) / 1024 * 1024;
   static constexpr int kP = kRing0 + kRing * kUnit;     // behind the ring: D = 64 reads one chunk past its last unit
   static constexpr int kMisc = kP + kPBufs * kPBytes;
-  static constexpr int kBytes = kMisc + NR * 18 + 256;
+  static constexpr int kBytes = kMisc + NR * 18 + 320;
   static constexpr int kO = 2 * NR;                     // TMEM columns: S0 [0, NR) S1 [NR, 2 NR) O [2 NR, (2 + kUnits) NR)
   static constexpr int kTmem = 4 * NR;
   static_assert(D != 256 || NR <= 64, "Q and P leave no room for the ring");
@@ -169,9 +172,11 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   uint64_t* p_full = s_empty + 2;      // [PB]
   uint64_t* p_empty = p_full + 2;      // [PB] P.V done
   uint64_t* drain = p_empty + 2;       // [2]
-  volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 2);
+  uint64_t* voted = drain + 2;         // [groups]
+  int* sOver = reinterpret_cast<int*>(voted + 4);  // [groups][2] tile number + 1 whose scores exceed a maximum by kLazy
+  volatile int* s_abort = reinterpret_cast<volatile int*>(sOver + 8);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
-  static_assert((2 * RING + 11) * 8 + 8 <= 256, "misc");
+  static_assert((2 * RING + 15) * 8 + 40 <= 320, "misc");
 
   // The merging kernel may be scheduled now: it waits for this grid to end.
   asm volatile("griddepcontrol.launch_dependents;");
@@ -187,10 +192,14 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], C::kSoftWarps * 32);
-      mbar_init(&p_full[i], C::kSoftWarps * 32);
+      mbar_init(&s_empty[i], C::kSoftWarps);
+      mbar_init(&p_full[i], C::kSoftWarps);
       mbar_init(&p_empty[i], 1);
       mbar_init(&drain[i], 1);
+    }
+    for (int i = 0; i < C::kGroups; ++i) {
+      mbar_init(&voted[i], 4);
+      sOver[2 * i] = sOver[2 * i + 1] = 0;
     }
     mbar_init(q_full, C::kSoftWarps * 32);
     *s_abort = 0;
@@ -206,7 +215,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   const uint32_t tmem = *s_tmem;
   const uint32_t ring = smem_u32(smem + C::kRing0);
 
-  if (warp == C::kSoftWarps + 2) {
+  if (warp >= C::kSoftWarps) {
+   if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+   if (warp == C::kSoftWarps + 2) {
     // =================== TMA producer ===================
     if (lane == 0) {
       uint32_t idx = 0;              // K (and V) units issued
@@ -238,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
           if (used >> i & 1) mbar_wait(&full[i], phase >> i & 1, &no_abort);
       }
     }
-  } else if (warp == C::kSoftWarps) {
+   } else if (warp == C::kSoftWarps) {
     // =================== S^T = K Q^T ===================
     constexpr uint32_t idesc = idesc_keys(NR, false);
     const uint32_t q_addr = smem_u32(smem + C::kQ);
@@ -269,7 +280,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     umma_commit(&drain[0]);
     volatile int no_abort = 0;
     mbar_wait(&drain[0], 0, &no_abort);
-  } else if (warp == C::kSoftWarps + 1) {
+   } else if (warp == C::kSoftWarps + 1) {
     // =================== O^T += V^T P^T ===================
     constexpr uint32_t idesc = idesc_keys(NR, true);
     bool ok = true;
@@ -297,7 +308,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     umma_commit(&drain[1]);
     volatile int no_abort = 0;
     mbar_wait(&drain[1], 0, &no_abort);
+   }
   } else {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // =================== softmax and epilogue: a thread per key ===================
     // A failed wait raises *s_abort and the thread runs on (every later wait
     // then fails at once): the barriers below need all of the group's threads.
@@ -323,16 +336,15 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       const __nv_bfloat16* src = p.q + b * p.qs[0] + static_cast<int64_t>(g) * p.G * p.qs[1] + qu * 8;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const int row = rt * NR + qr + k * kStep;
-        const int t = row / p.G, h = row - t * p.G;
-        y[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < p.R) y[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
+        const int row = min(rt * NR + qr + k * kStep, p.R - 1), t = row / p.G, h = row - t * p.G;
+        y[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
       }
     };
-    auto store_q = [&](const uint4 (&y)[kPer]) {
+    auto store_q = [&](uint4 (&y)[kPer]) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         const int r = qr + k * kStep;
+        if (rt * NR + r >= p.R) y[k] = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(smem + C::kQ + (qu >> 3) * (NR * 128) + r * 128 + (((qu & 7) ^ (r & 7)) << 4)) = y[k];
       }
       fence_proxy_async_smem();
@@ -343,7 +355,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     fetch_q(w.b, w.g, qy);
     store_q(qy);
     int n = 0;
-    bool more;
+    uint32_t votes = 0;
+    bool more = false;
     do {
       const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
       if (tid < W) {
@@ -363,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       for (int c = 0; c < W / 2; ++c) l[c] = 0ull;
 
       Walk nx = w;
-      more = nx.next(ln);
+      if (kEarlyQ) more = nx.next(ln);
       for (int t = w.t0; t < w.t1; ++t, ++n) {
         const int base = t * kKeys;
         const uint32_t st = tm + (n & 1) * NR;  // the scores
@@ -454,14 +467,16 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
               for (int i = 0; i < D / U / 8; ++i) vrow[u][(i >> 3) * (kChunk / 16) + (i & 7)] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        // ---- scores in powers of two, relative to the rows' maxima ----
-        // A pair's first tile sets them; a row may still have none in a tile
-        // of drafted keys only. Otherwise they move when a score exceeds one
-        // by more than kLazy.
+        // ---- weights 2^x of the scores x in powers of two relative to the rows'
+        // maxima, and P in bf16 ----
+        // A pair's first tile sets the maxima; a row may still have none in a
+        // tile of drafted keys only. Otherwise they move when a score exceeds
+        // one by more than kLazy: the warps vote on that while they compute the
+        // weights, and compute them again where one says so.
         float x[W];
         bool renew = t == w.t0 || base >= w.len;
 #pragma unroll 1
-        for (bool again = false;; again = true) {
+        for (bool again = renew;; again = true) {
           if (renew) {
             tmem_ld_cols<W>(st, x);
 #pragma unroll
@@ -519,31 +534,50 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
             mx[0] = fmax3(mx[0], x[c], x[c + 1]);
             mx[1] = fmax3(mx[1], x[c + 2], x[c + 3]);
           }
-          if (renew || again) break;
-          renew = vote_or(bar, fmaxf(mx[0], mx[1]) > kLazy);
+          if (!again) {
+            const bool over = __any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > kLazy);
+            if (lane == 0) {
+              if (over) sOver[2 * grp + (n & 1)] = n + 1;
+              mbar_arrive(&voted[grp]);
+            }
+          }
+          if (n >= PB) mbar_wait(&p_empty[n % PB], ((n / PB) - 1) & 1, s_abort);
+          uint8_t* prow = pbuf + (col0 >> 6) * kChunk + tid * 128;
+#pragma unroll
+          for (int u = 0; u < W / 8; ++u) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float& e0 = x[u * 8 + 2 * i];
+              float& e1 = x[u * 8 + 2 * i + 1];
+              e0 = ex2_approx(e0);
+              e1 = ex2_approx(e1);
+              pk[i] = pack_bf16x2(e0, e1);
+            }
+            *reinterpret_cast<uint4*>(prow + ((((col0 & 63) / 8 + u) ^ (tid & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+          if (again) break;
+          mbar_wait(&voted[grp], votes & 1, s_abort);
+          ++votes;
+          renew = *reinterpret_cast<volatile int*>(&sOver[2 * grp + (n & 1)]) == n + 1;
           if (!renew) break;
         }
+#pragma unroll
+        for (int c = 0; c < W / 2; ++c) l[c] = f2_add(l[c], f2_pack(x[2 * c], x[2 * c + 1]));
         tc_fence_before();
-        mbar_arrive(&s_empty[n & 1]);
-        // ---- weights 2^x, their sums, and P in bf16 ----
-        uint32_t pk[W / 2];
-#pragma unroll
-        for (int c = 0; c < W / 2; ++c) {
-          const float e0 = ex2_approx(x[2 * c]), e1 = ex2_approx(x[2 * c + 1]);
-          l[c] = f2_add(l[c], f2_pack(e0, e1));
-          pk[c] = pack_bf16x2(e0, e1);
-        }
-        if (n >= PB) mbar_wait(&p_empty[n % PB], ((n / PB) - 1) & 1, s_abort);
-        uint8_t* prow = pbuf + (col0 >> 6) * kChunk + tid * 128;
-#pragma unroll
-        for (int u = 0; u < W / 8; ++u)
-          *reinterpret_cast<uint4*>(prow + ((((col0 & 63) / 8 + u) ^ (tid & 7)) << 4)) =
-              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
         fence_proxy_async_smem();
-        mbar_arrive(&p_full[n % PB]);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s_empty[n & 1]);
+          mbar_arrive(&p_full[n % PB]);
+        }
       }
 
       // Q of the next pair now: every S of this one is done.
+      if (!kEarlyQ) {
+        nx = w;
+        more = nx.next(ln);
+      }
       if (more) {
         if (!kEarlyQ) fetch_q(nx.b, nx.g, qy);
         store_q(qy);
