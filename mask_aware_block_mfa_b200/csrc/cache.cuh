@@ -33,15 +33,30 @@ __device__ __forceinline__ bool tree_sees(const int32_t* par, int t, int n) {
   return a == n;
 }
 
+// Division of numbers below 2^31 by a divisor known on the host: with
+// 2^(shift - 1) < d <= 2^shift and mul = ceil(2^(31 + shift) / d), n mul / 2^(31 + shift)
+// exceeds n / d by less than n / 2^31 / d < 1 / d.
+struct FastDiv {
+  uint32_t mul, shift;
+  __host__ void set(uint32_t d) {
+    shift = 0;
+    while ((uint64_t(1) << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((uint64_t(1) << (31 + shift)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> (31 + shift));
+  }
+};
+
 // Which of the X rows from `first` on (row = node * G + head) see the key of `node`, as
 // bits: in a chain the rows from first + from on; in a tree by the table
 // seen[T][words] of the nodes each node sees.
 __device__ __forceinline__ uint32_t rows_from(int from) { return from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from; }
 template <int X>
-__device__ __forceinline__ uint32_t rows_seeing(const uint32_t* seen, int words, int node, int first, int G, int T) {
+__device__ __forceinline__ uint32_t rows_seeing(const uint32_t* seen, int words, int node, int first, int G, FastDiv by_g, int T) {
   uint32_t bits = 0u;
   const uint32_t* col = seen + (node >> 5);
-  const int t0 = first / G, t1 = min((first + X - 1) / G, T - 1);
+  const int t0 = by_g(first), t1 = min(by_g(first + X - 1), T - 1);
 #pragma unroll 4
   for (int t = t0; t <= t1; ++t) {
     const uint32_t yes = (col[t * words] >> (node & 31)) & 1u;

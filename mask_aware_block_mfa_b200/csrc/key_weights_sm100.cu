@@ -31,6 +31,7 @@ constexpr int kSmem = 232448;
 
 struct KeyWeightParams {
   int32_t B, Hq, Hkv, G, T, N, R;
+  FastDiv by_g;
   int32_t row0, qtiles;          // rows of this pass: row0 .., in qtiles (1 or 2) tiles of NR
   int32_t ring, words, ctas;     // K units; 32-bit words of a row's nodes; CTAs of the line
   float scale_log2, decay, unscale;  // unscale: 1 / scale_log2
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool real = i < p.qtiles * NR;
         float c = -1e30f, sign = 0.f;
         if (real && row < p.R) {
-          const int t = row / p.G, h = w.g * p.G + row - t * p.G;
+          const int t = p.by_g(row), h = w.g * p.G + row - t * p.G;
           const float lse = __ldg(p.lse + (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t);
           const float scale = p.row_scale ? __ldg(p.row_scale + static_cast<int64_t>(w.b) * p.T + t) : 1.f;
           const int up = par ? __ldg(par + t) : 0;
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 x[kBatch];
 #pragma unroll
           for (int y = 0; y < kBatch; ++y) {
-            const int row = min(p.row0 + i0 + y * kStep, p.R - 1), t = row / p.G, h = row - t * p.G;
+            const int row = min(p.row0 + i0 + y * kStep, p.R - 1), t = p.by_g(row), h = row - t * p.G;
             x[y] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
           }
 #pragma unroll
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < NR; c += X) {
             const int first = p.row0 + rt * NR + c;
             uint32_t see = (sActive[(rt * NR + c) >> 5] >> (c & 31)) & (X == 32 ? ~0u : (1u << X) - 1u);
-            if (j >= w.len) see = j < end ? see & (par ? rows_seeing<X>(sSeen, p.words, node, first, p.G, p.T) : rows_from(node * p.G - first)) : 0u;
+            if (j >= w.len) see = j < end ? see & (par ? rows_seeing<X>(sSeen, p.words, node, first, p.G, p.by_g, p.T) : rows_from(node * p.G - first)) : 0u;
             uint32_t x[X];
             if constexpr (X == 16) tmem_ld_32x32b_x16(st + c, x);
             else tmem_ld_32x32b_x32(st + c, x);
@@ -417,6 +418,7 @@ extern "C" mfa_status mfa_key_weights(const mfa_tensor* q, const mfa_tensor* k, 
   p.B = static_cast<int32_t>(q->B); p.Hq = static_cast<int32_t>(q->H); p.Hkv = static_cast<int32_t>(k->H);
   p.G = static_cast<int32_t>(q->H / k->H); p.T = static_cast<int32_t>(q->N); p.N = static_cast<int32_t>(k->N);
   p.R = p.T * p.G;
+  p.by_g.set(static_cast<uint32_t>(p.G));
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(q->D)));
   p.unscale = static_cast<float>(std::sqrt(static_cast<double>(q->D)) / 1.4426950408889634);
   p.decay = decay;

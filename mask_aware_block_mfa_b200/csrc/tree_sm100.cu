@@ -24,6 +24,7 @@
 // pair cut between CTAs each writes an unnormalised part (m, l, o), and a
 // dependent launch merges them in a fixed order.
 #include <cfloat>
+#include <climits>
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -39,6 +40,7 @@ constexpr float kLazy = 8.0f;        // a row's maximum moves when a score excee
 
 struct TreeParams {
   int32_t B, Hq, Hkv, G, T, N, R;  // R = T * G rows per key/value head
+  FastDiv by_g;
   int32_t rtiles, groups;          // row tiles; CTAs per row tile
   float scale_log2;
   const __nv_bfloat16* q;
@@ -51,7 +53,7 @@ struct TreeParams {
 
 template <int NR>
 __device__ __forceinline__ int last_node(const TreeParams& p, int rt) {
-  return min((rt * NR + NR - 1) / p.G, p.T - 1);
+  return min(p.by_g(rt * NR + NR - 1), p.T - 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -81,7 +83,7 @@ struct Cfg {
   static constexpr int kRing0 = (kQBytes + 1023) / 1024 * 1024;
   static constexpr int kP = kRing0 + kRing * kUnit;     // behind the ring: D = 64 reads one chunk past its last unit
   static constexpr int kMisc = kP + kPBufs * kPBytes;
-  static constexpr int kBytes = kMisc + NR * 18 + 320;
+  static constexpr int kBytes = kMisc + NR * 17 + 360;
   static constexpr int kO = 2 * NR;                     // TMEM columns: S0 [0, NR) S1 [NR, 2 NR) O [2 NR, (2 + kUnits) NR)
   static constexpr int kTmem = 4 * NR;
   static_assert(D != 256 || NR <= 64, "Q and P leave no room for the ring");
@@ -162,8 +164,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   float* sAlpha = sDelta + NR;                               // [NR] what its sums are multiplied by as its maximum moves
   float* sRed = sAlpha + NR;                                 // [NR] with sDelta and sAlpha: what warps 1 to 3 of a group hand to warp 0
   uint8_t* sSet = reinterpret_cast<uint8_t*>(sRed + NR);     // [NR] the row has a maximum
-  uint8_t* sPoison = sSet + NR;                              // [NR] the row sees a value that is not finite
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sPoison + NR);
+  uint32_t* sBad = reinterpret_cast<uint32_t*>(sSet + NR);   // [kSeenWords] a tree's nodes whose values are not finite,
+  int* sBadMin = reinterpret_cast<int*>(sBad + kSeenWords);  // [2] a chain's first one (INT_MAX: none; a tree: any below that)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sBadMin + 2);
   uint64_t* full = bars;               // [RING]
   uint64_t* empty = full + RING;       // [RING]
   uint64_t* q_full = empty + RING;     // Q of the next pair is in shared memory
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   int* sOver = reinterpret_cast<int*>(voted + 4);  // [groups][2] tile number + 1 whose scores exceed a maximum by kLazy
   volatile int* s_abort = reinterpret_cast<volatile int*>(sOver + 8);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
-  static_assert((2 * RING + 15) * 8 + 40 <= 320, "misc");
+  static_assert(40 + (2 * RING + 15) * 8 + 40 <= 360, "misc");
 
   // The merging kernel may be scheduled now: it waits for this grid to end.
   asm volatile("griddepcontrol.launch_dependents;");
@@ -185,6 +188,21 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   if (start.b < 0) return;  // more CTAs than places
   Walk w(ln, start, p.groups);
   if (!w.more) return;      // none of them a tile
+  // Q of a pair, zeros for rows that are none. (A padding row's Q may be
+  // anything: it reaches no other row.)
+  constexpr int kPer = NR * (D / 8) / (C::kSoftWarps * 32), kStep = C::kSoftWarps * 32 / (D / 8);
+  const int qu = threadIdx.x % (D / 8), qr = threadIdx.x / (D / 8);
+  auto fetch_q = [&](int b, int g, uint4 (&y)[kPer]) {
+    const __nv_bfloat16* src = p.q + b * p.qs[0] + static_cast<int64_t>(g) * p.G * p.qs[1] + qu * 8;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int row = min(rt * NR + qr + k * kStep, p.R - 1), t = p.by_g(row), h = row - t * p.G;
+      y[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
+    }
+  };
+  constexpr bool kEarlyQ = NR < 128;  // the next pair's during the last tile (where the registers allow it)
+  uint4 qy[kPer];
+  if (warp < C::kSoftWarps) fetch_q(w.b, w.g, qy);
   if (threadIdx.x == 0) {
     for (int i = 0; i < RING; ++i) {
       mbar_init(&full[i], 1);
@@ -194,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], C::kSoftWarps);
       mbar_init(&p_full[i], C::kSoftWarps);
-      mbar_init(&p_empty[i], 1);
+      mbar_init(&p_empty[i], 2);
       mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < C::kGroups; ++i) {
@@ -290,6 +308,57 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         const uint32_t first = static_cast<uint32_t>(n) * U;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_full[n % PB], (n / PB) & 1, s_abort)))) break;
         const uint32_t pb = sdesc_sw128_lo(smem_u32(smem + C::kP) + (n % PB) * C::kPBytes, kChunk);
+        if (t == w.t0) {
+          if (lane < kSeenWords) sBad[lane] = 0u;
+          if (lane == 0) *sBadMin = INT_MAX;
+          __syncwarp();
+        }
+        if (t * kKeys + kKeys > w.len) {
+          // V of a key that is not before the sequence's end must be finite, seen or
+          // not: 0 * inf would reach every row. Rows that are not become zeros, and
+          // the rows of the output that see one become NaN in the epilogue.
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[RK + (first + u) % RV], ((first + u) / RV) & 1, s_abort));
+          if (!ok) break;
+          constexpr int kWide = D < 128 ? D / 8 : 16, kAtOnce = 32 / kWide;  // 16-byte units of a row in a ring unit; rows
+          const int begin = max(w.len - t * kKeys, 0), end = min(min(w.len + p.T, p.N) - t * kKeys, kKeys);
+          const int c = lane % kWide;
+          auto at = [&](int u, int r) {
+            return reinterpret_cast<uint4*>(smem + C::kRing0 + (RK + (first + u) % RV) * C::kUnit + (c >> 3) * kChunk + r * 128 + (c & 7) * 16);
+          };
+#pragma unroll 2
+          for (int r0 = begin; r0 < end; r0 += kAtOnce) {
+            const int r = r0 + lane / kWide;
+            uint32_t bad = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const uint4 y = r < end ? *at(u, r) : make_uint4(0u, 0u, 0u, 0u);
+              bad |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u)) |
+                     (__vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u));
+            }
+            const unsigned lanes = __ballot_sync(0xffffffffu, bad != 0);
+            if (lanes >> (lane / kWide * kWide) & ((1u << (kWide - 1)) * 2u - 1u)) {
+#pragma unroll
+              for (int u = 0; u < U; ++u) *at(u, r) = make_uint4(0u, 0u, 0u, 0u);
+              if (c == 0) {
+                const int node = t * kKeys + r - w.len;
+                if (p.parents) atomicOr(sBad + (node >> 5), 1u << (node & 31));
+                atomicMin(sBadMin, node);
+              }
+            }
+          }
+#pragma unroll 4
+          for (int r0 = max(end, begin); r0 < kKeys; r0 += kAtOnce) {
+            const int r = r0 + lane / kWide;
+            if (r < kKeys) {
+#pragma unroll
+              for (int u = 0; u < U; ++u) *at(u, r) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const uint32_t slot = RK + (first + u) % RV;
@@ -303,6 +372,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
           umma_commit(&empty[slot]);
         }
         umma_commit(&p_empty[n % PB]);
+        if (lane == 0) mbar_arrive(&p_empty[n % PB]);  // (orders sBad before the epilogue)
       }
     } while (ok && w.next(ln));
     umma_commit(&drain[1]);
@@ -328,18 +398,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     // Row col0 + c's slot of warp `quad` (1 to 3).
     float* slot = (quad == 1 ? sRed : quad == 2 ? sDelta : sAlpha) + col0;
     const float* red = sRed + col0;
-    // Q of a pair, zeros for rows that are none. (A padding row's Q may be
-    // anything: it reaches no other row.)
-    constexpr int kPer = NR * (D / 8) / (C::kSoftWarps * 32), kStep = C::kSoftWarps * 32 / (D / 8);
-    const int qu = threadIdx.x % (D / 8), qr = threadIdx.x / (D / 8);
-    auto fetch_q = [&](int b, int g, uint4 (&y)[kPer]) {
-      const __nv_bfloat16* src = p.q + b * p.qs[0] + static_cast<int64_t>(g) * p.G * p.qs[1] + qu * 8;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int row = min(rt * NR + qr + k * kStep, p.R - 1), t = row / p.G, h = row - t * p.G;
-        y[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
-      }
-    };
     auto store_q = [&](uint4 (&y)[kPer]) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
@@ -350,9 +408,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     };
-    constexpr bool kEarlyQ = NR < 128;  // (where the registers allow it)
-    uint4 qy[kPer];
-    fetch_q(w.b, w.g, qy);
     store_q(qy);
     int n = 0;
     uint32_t votes = 0;
@@ -362,7 +417,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       if (tid < W) {
         negM[tid] = 0.f;
         sSet[col0 + tid] = 0;
-        sPoison[col0 + tid] = 0;
       }
       if (rt == 0 && w.g == 0 && w.t0 == 0) {
         for (int t = threadIdx.x; t < (par ? p.T : 1); t += C::kSoftWarps * 32) {
@@ -384,89 +438,45 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         uint8_t* pbuf = smem + C::kP + (n % PB) * C::kPBytes;
         mbar_wait(&s_full[n & 1], (n >> 1) & 1, s_abort);
         tc_fence_after();
-        if (base + kKeys > w.len) {
+        const bool draft = base + kKeys > w.len;
+        uint32_t see = ~0u;  // rows that see this thread's key, as bits
+        if (draft) {
           // ---- a tile with drafted keys, or the last: who sees what ----
-          // P's buffer is free (the wait passes while it was never used); its
-          // slice of the group holds the parents and the nodes each row sees.
-          mbar_wait(&p_empty[n % PB], ((n / PB) - 1) & 1, s_abort);
           const int j = base + tid, node = j - w.len;
-          const bool held = j < min(w.len + p.T, p.N);
-          int* sPar = reinterpret_cast<int*>(pbuf + grp * (C::kPBytes / C::kGroups));
-          uint32_t* sSeen = reinterpret_cast<uint32_t*>(sPar + MFA_TREE_MAX_NODES);  // [W][kSeenWords]
-          if (par) {
+          if (j >= min(w.len + p.T, p.N)) see = 0u;
+          if (!par) {
+            if (j >= w.len) see &= rows_from(node * p.G - row0);
+          } else {
+            // P's buffer is free (the wait passes while it was never used); its
+            // slice of the group holds the parents and the nodes each row sees.
+            mbar_wait(&p_empty[n % PB], ((n / PB) - 1) & 1, s_abort);
+            int* sPar = reinterpret_cast<int*>(pbuf + grp * (C::kPBytes / C::kGroups));
+            uint32_t* sSeen = reinterpret_cast<uint32_t*>(sPar + MFA_TREE_MAX_NODES);  // [W][kSeenWords]
             for (int i = tid; i < p.T; i += 128) sPar[i] = __ldg(par + i);
             for (int i = tid; i < W * kSeenWords; i += 128) sSeen[i] = 0u;
             named_barrier(bar, 128);
             if (tid < rows && tid < W) {
-              const int tt = (row0 + tid) / p.G;
+              const int tt = p.by_g(row0 + tid);
               for (int a = sPar[tt] == -2 ? -1 : tt; a >= 0; a = tree_up(sPar, a))
                 sSeen[tid * kSeenWords + (a >> 5)] |= 1u << (a & 31);
             }
             named_barrier(bar, 128);
-          }
-          // V of a key that is not before the sequence's end must be finite,
-          // seen or not: 0 * inf would reach every row. (These threads have not
-          // followed the V ring's phases. Its slot's last unit is over when the P.V
-          // that read it is done: three tiles back, awaited for P's buffer, or, with
-          // two units to a tile, the tile before.)
-          if (U == 2 && n > 0) mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
-          uint4* vrow[U];
-          bool finite = true;
-          if (j >= w.len) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const uint32_t unit = static_cast<uint32_t>(n) * U + u, slot = RK + unit % RV;
-              mbar_wait(&full[slot], (unit / RV) & 1, s_abort);
-              vrow[u] = reinterpret_cast<uint4*>(smem + C::kRing0 + slot * C::kUnit + tid * 128);
-            }
-            if (held) {
-              uint32_t bad = 0;
-#pragma unroll
-              for (int u = 0; u < U; ++u)
-#pragma unroll 8
-                for (int i = 0; i < D / U / 8; ++i) {
-                  const uint4 y = vrow[u][(i >> 3) * (kChunk / 16) + (i & 7)];
-                  bad |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u)) |
-                         (__vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u));
-                }
-              finite = bad == 0;
-            }
-          }
-          uint32_t see = rows >= W ? ~0u : rows > 0 ? (1u << rows) - 1u : 0u;  // rows that see key j, as bits
-          if (j >= w.len) {
-            if (!held) {
+            if (j >= w.len && see != 0u) {
               see = 0u;
-            } else if (par) {
-              uint32_t bits = 0u;
-#pragma unroll 8
-              for (int c = 0; c < W; ++c) bits |= ((sSeen[c * kSeenWords + (node >> 5)] >> (node & 31)) & 1u) << c;
-              see &= bits;
-            } else {
-              see &= rows_from(node * p.G - row0);
+#pragma unroll
+              for (int c = 0; c < W; ++c) see |= ((sSeen[c * kSeenWords + (node >> 5)] >> (node & 31)) & 1u) << c;
             }
-            if (!finite)
-              for (int c = 0; c < W; ++c)
-                if (see >> c & 1) sPoison[col0 + c] = 1;
-          }
-#pragma unroll 1
-          for (int c = 0; c < W; c += 16) {
-            uint32_t x[16];
-            tmem_ld_32x32b_x16(st + c, x);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (j >= w.len && !(see >> (c + i) & 1)) x[i] = 0xff800000u;
-            tmem_st_32x32b_x16(st + c, x);
-          }
-          tmem_st_wait();
-          named_barrier(kAll, C::kSoftWarps * 32);  // every group has looked
-          if (j >= w.len && !(held && finite) && grp == 0) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll 8
-              for (int i = 0; i < D / U / 8; ++i) vrow[u][(i >> 3) * (kChunk / 16) + (i & 7)] = make_uint4(0u, 0u, 0u, 0u);
+            named_barrier(kAll, C::kSoftWarps * 32);  // every group has looked: P may be written
           }
         }
+        auto scores = [&](float (&y)[W]) {
+          tmem_ld_cols<W>(st, y);
+          if (draft) {
+#pragma unroll
+            for (int c = 0; c < W; ++c)
+              if (!(see >> c & 1)) y[c] = -INFINITY;
+          }
+        };
         // ---- weights 2^x of the scores x in powers of two relative to the rows'
         // maxima, and P in bf16 ----
         // A pair's first tile sets the maxima; a row may still have none in a
@@ -478,7 +488,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 #pragma unroll 1
         for (bool again = renew;; again = true) {
           if (renew) {
-            tmem_ld_cols<W>(st, x);
+            scores(x);
 #pragma unroll
             for (int c = 0; c < W; ++c) x[c] = fmaf(x[c], p.scale_log2, negM[c]);
             float m = warp_reduce_spread<W>(x, lane, [](float a, float b) { return fmaxf(a, b); });
@@ -523,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
               tmem_st_wait();
             }
           }
-          tmem_ld_cols<W>(st, x);
+          scores(x);
           const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
           float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -588,6 +598,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * NR + col0;
       float part_sum;
       named_barrier(bar, 128);  // the last tile's alpha has been read
+      mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);  // O and sBad are complete
+      tc_fence_after();
       {
         float v[W];
 #pragma unroll
@@ -598,12 +610,19 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       }
       named_barrier(bar, 128);
       if (tid < rows && tid < W) {
-        const int tt = (row0 + tid) / p.G, h = w.g * p.G + (row0 + tid) % p.G;
+        const int tt = p.by_g(row0 + tid), h = w.g * p.G + row0 + tid - tt * p.G;
         const bool dead = par && __ldg(par + tt) == -2;
         const float sum = dead ? 0.f : (part_sum + red[tid]) + (delta[tid] + alpha[tid]);
         const float m = -negM[tid];
+        // Does the row see a node whose values are not finite? (Not dead: the row's way up is
+        // the one its keys were masked by.)
+        bool poison = *sBadMin <= tt;
+        if (poison && par) {
+          poison = false;
+          for (int a = tt; a >= 0; a = tree_up(par, a)) poison |= sBad[a >> 5] >> (a & 31) & 1u;
+        }
         // -1: no output.
-        delta[tid] = sum == 0.f ? -1.f : (sPoison[col0 + tid] ? NAN : (whole ? 1.f / sum : 1.f));
+        delta[tid] = sum == 0.f ? -1.f : (poison ? NAN : (whole ? 1.f / sum : 1.f));
         if (whole) {
           p.lse[(static_cast<int64_t>(w.b) * p.Hq + h) * p.T + tt] =
               sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
@@ -616,8 +635,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         reinterpret_cast<int*>(alpha)[tid] = static_cast<int>(to >> 32);
       }
       named_barrier(bar, 128);
-      mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
-      tc_fence_after();
 #pragma unroll 1
       for (int k = 0; k < U * (W / 16); ++k) {
         const int u = k / (W / 16), c0 = (k % (W / 16)) * 16;
@@ -745,7 +762,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
 #pragma unroll
       for (int x = 1; x < kMergeWarps; ++x) o[e] += so[x][lane * E + e];
   }
-  const int row = rt * NR + r, t = row / p.G, h = g * p.G + row % p.G;
+  const int row = rt * NR + r, t = p.by_g(row), h = g * p.G + row - t * p.G;
   const bool has = l != 0.f;
   const float inv = has ? 1.f / l : 0.f;
   uint32_t* to = reinterpret_cast<uint32_t*>(p.out + b * p.os[0] + h * p.os[1] + t * p.os[2] + lane * E);
@@ -862,6 +879,7 @@ extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, 
   p.B = static_cast<int32_t>(q->B); p.Hq = static_cast<int32_t>(q->H); p.Hkv = static_cast<int32_t>(k->H);
   p.G = static_cast<int32_t>(q->H / k->H); p.T = static_cast<int32_t>(q->N); p.N = static_cast<int32_t>(k->N);
   p.R = static_cast<int32_t>(R);
+  p.by_g.set(static_cast<uint32_t>(p.G));
   p.rtiles = pl.rtiles; p.groups = pl.groups;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(q->D)));
   p.q = static_cast<const __nv_bfloat16*>(q->data);
