@@ -174,6 +174,23 @@ __host__ __device__ constexpr uint32_t idesc_keys(int N, bool mn_major) {
 
 // ---- host ----
 
+// A launch that may begin while the kernel before it in the stream ends (the
+// kernel waits for that one, griddepcontrol.wait, before it reads anything).
+template <typename... P, typename... A>
+inline bool launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
 // A [B, H, N, D] bf16 tensor as these operators take it: D contiguous, the
 // other strides and the address on 16 bytes (the kernels' wide and TMA loads).
 inline mfa_status check_cache_tensor(const mfa_tensor* t) {

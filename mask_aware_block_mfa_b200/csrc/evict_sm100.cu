@@ -381,23 +381,6 @@ __global__ void __launch_bounds__(kMoveThreads) mfa_compact_in_place_kernel(cons
   }
 }
 
-// A launch that may begin while the kernel before it in the stream ends (it waits for that
-// kernel before it reads anything).
-template <typename P>
-bool launch_after(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
-}
-
 // The bytes of a [B, H, N, ...] tensor, first to last, as an address range.
 struct Range {
   uintptr_t lo, hi;

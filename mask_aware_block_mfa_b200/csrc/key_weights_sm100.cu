@@ -82,12 +82,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* sPar = s_minus + 1;                                             // [T] the tree
   uint32_t* sSeen = reinterpret_cast<uint32_t*>(sPar + p.T);           // [T][words] the nodes each one sees
 
-  const Line ln{p.lens, p.B, p.Hkv, p.N, p.T - 1, C::kExtra};
-  const Start start = find_start(ln, blockIdx.x, p.ctas);
-  if (start.b < 0) return;  // more CTAs than places
-  Walk w(ln, start, p.ctas);
-  if (!w.more) return;      // none of them a tile
-  if (threadIdx.x == 0) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (warp == kGroups * 4 + 1 && lane == 0) {
+    tma_prefetch_desc(&tm_k);
     for (int i = 0; i < p.ring; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -102,6 +99,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     *s_minus = 0;
     fence_mbarrier_init();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Line ln{p.lens, p.B, p.Hkv, p.N, p.T - 1, C::kExtra};
+  const Start start = find_start(ln, blockIdx.x, p.ctas);
+  if (start.b < 0) return;  // more CTAs than places
+  Walk w(ln, start, p.ctas);
+  if (!w.more) return;      // none of them a tile
+  // What a pair's rows need from memory, fetched together: a thread's row (its
+  // lse, scale and parent) and its part of the first kBatch steps of Q.
+  constexpr int kStep = kSoftThreads / (D / 8), kBatch = NR < kStep ? 1 : NR / kStep < 4 ? NR / kStep : 4;
+  const int qu = threadIdx.x % (D / 8), qr = threadIdx.x / (D / 8);
+  struct {
+    float lse, scale;
+    int up;
+    uint4 q[kBatch];
+  } pre;
+  auto fetch_q = [&](int i0) {
+    const __nv_bfloat16* src = p.q + w.b * p.qs[0] + static_cast<int64_t>(w.g) * p.G * p.qs[1] + qu * 8;
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int row = min(p.row0 + i0 + y * kStep, p.R - 1), t = p.by_g(row), h = row - t * p.G;
+      pre.q[y] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
+    }
+  };
+  auto fetch = [&]() {
+    const int row = min(p.row0 + static_cast<int>(threadIdx.x), p.R - 1), t = p.by_g(row), h = w.g * p.G + row - t * p.G;
+    pre.lse = __ldg(p.lse + (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t);
+    pre.scale = p.row_scale ? __ldg(p.row_scale + static_cast<int64_t>(w.b) * p.T + t) : 1.f;
+    pre.up = p.parents ? __ldg(p.parents + static_cast<int64_t>(w.b) * p.T + t) : 0;
+    fetch_q(qr);
+  };
+  if (threadIdx.x < kSoftThreads) fetch();
+  int slot = 0, round = 0;  // the TMA producer's and the MMA issuer's: of the next unit
+  // K of tile t; false when a wait ran out.
+  auto load_tile = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1, s_abort)) return false;
+      mbar_arrive_expect_tx(&full[slot], C::kUnit);
+#pragma unroll
+      for (int c = 0; c < C::kUnit / kChunk; ++c)
+        tma_load_4d(smem + slot * C::kUnit + c * kChunk, &tm_k, &full[slot], u * 128 + c * 64, t * kKeys, w.g, w.b);
+      if (++slot == p.ring) {
+        slot = 0;
+        ++round;
+      }
+    }
+    return true;
+  };
+  if (warp == kGroups * 4 + 1 && lane == 0) load_tile(w.t0);
   if (warp == kGroups * 4) {
     tmem_alloc(s_tmem, kGroups * NR);
     tmem_relinquish();
@@ -114,24 +160,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kGroups * 4 + 1) {
     // =================== TMA producer ===================
     if (lane == 0) {
-      int slot = 0, round = 0;  // of the next unit
       bool ok = true;
-      do {
-        for (int t = w.t0; t < w.t1 && ok; ++t) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (round > 0 && !(ok = mbar_wait(&empty[slot], (round - 1) & 1, s_abort))) break;
-            mbar_arrive_expect_tx(&full[slot], C::kUnit);
-#pragma unroll
-            for (int c = 0; c < C::kUnit / kChunk; ++c)
-              tma_load_4d(smem + slot * C::kUnit + c * kChunk, &tm_k, &full[slot], u * 128 + c * 64, t * kKeys, w.g, w.b);
-            if (++slot == p.ring) {
-              slot = 0;
-              ++round;
-            }
-          }
-        }
-      } while (ok && w.next(ln));
+      for (int t = w.t0 + 1; t < w.t1 && ok; ++t) ok = load_tile(t);
+      while (ok && w.next(ln))
+        for (int t = w.t0; t < w.t1 && ok; ++t) ok = load_tile(t);
       if (*s_abort) {
         // Loads in flight land before the CTA exits.
         volatile int no_abort = 0;
@@ -148,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring = smem_u32(smem), q_addr = smem_u32(sQ);
     bool ok = true;
     uint32_t item = 0;
-    int slot = 0, round = 0, seg = 0;
+    int seg = 0;
     do {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(q_full, seg & 1, s_abort));
       for (int t = w.t0; t < w.t1 && ok; ++t) {
@@ -210,25 +242,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int n = 0;           // tiles of the CTA so far
     int k = 0;           // of them the group's
+    bool begun = false;
     do {
+      if (begun) fetch();
+      begun = true;
       const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
       // ---- the pair's rows (all of the last pair's S and sums are done) ----
       // Rows that count for nothing, whatever they hold, become Q = 0 with a constant that
       // no exponential survives.
       {
-        const int i = threadIdx.x, row = p.row0 + i, r = i % NR, q = i / NR;
+        const int i = threadIdx.x, r = i % NR, q = i / NR;
         const bool real = i < p.qtiles * NR;
         float c = -1e30f, sign = 0.f;
-        if (real && row < p.R) {
-          const int t = p.by_g(row), h = w.g * p.G + row - t * p.G;
-          const float lse = __ldg(p.lse + (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t);
-          const float scale = p.row_scale ? __ldg(p.row_scale + static_cast<int64_t>(w.b) * p.T + t) : 1.f;
-          const int up = par ? __ldg(par + t) : 0;
-          if (scale != 0.f && lse != -INFINITY && up != -2) {
-            sign = scale < 0.f ? -1.f : 1.f;
-            if (scale < 0.f) *s_minus = 1;
-            c = (log2f(fabsf(scale)) - lse * 1.4426950408889634f) * p.unscale;  // in the scores' unit
-          }
+        if (real && p.row0 + i < p.R && pre.scale != 0.f && pre.lse != -INFINITY && pre.up != -2) {
+          sign = pre.scale < 0.f ? -1.f : 1.f;
+          if (pre.scale < 0.f) *s_minus = 1;
+          c = (log2f(fabsf(pre.scale)) - pre.lse * 1.4426950408889634f) * p.unscale;  // in the scores' unit
         }
         const unsigned active = __ballot_sync(0xffffffffu, sign != 0.f);
         if (lane == 0 && real) sActive[warp] = active;
@@ -261,24 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int a = sPar[t] == -2 ? -1 : t; a >= 0; a = tree_up(sPar, a)) sSeen[t * p.words + (a >> 5)] |= 1u << (a & 31);
         }
       }
-      {
-        const int u = threadIdx.x % (D / 8);
-        const __nv_bfloat16* src = p.q + w.b * p.qs[0] + static_cast<int64_t>(w.g) * p.G * p.qs[1] + u * 8;
-        constexpr int kStep = kSoftThreads / (D / 8), kBatch = NR < kStep ? 1 : NR / kStep < 4 ? NR / kStep : 4;  // rows at a time
-        for (int i0 = threadIdx.x / (D / 8); i0 < p.qtiles * NR; i0 += kBatch * kStep) {
-          uint4 x[kBatch];
+      for (int i0 = qr; i0 < p.qtiles * NR; i0 += kBatch * kStep) {
+        if (i0 != qr) fetch_q(i0);
 #pragma unroll
-          for (int y = 0; y < kBatch; ++y) {
-            const int row = min(p.row0 + i0 + y * kStep, p.R - 1), t = p.by_g(row), h = row - t * p.G;
-            x[y] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
-          }
-#pragma unroll
-          for (int y = 0; y < kBatch; ++y) {
-            const int i = i0 + y * kStep, r = i % NR;
-            if (i >= p.qtiles * NR) break;
-            if (sSign[i] == 0.f) x[y] = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(sQ + (i / NR) * C::kQTile + (u >> 3) * (NR * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x[y];
-          }
+        for (int y = 0; y < kBatch; ++y) {
+          const int i = i0 + y * kStep, r = i % NR;
+          if (i >= p.qtiles * NR) break;
+          if (sSign[i] == 0.f) pre.q[y] = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(sQ + (i / NR) * C::kQTile + (qu >> 3) * (NR * 128) + r * 128 + (((qu & 7) ^ (r & 7)) << 4)) = pre.q[y];
         }
       }
       fence_proxy_async_smem();
@@ -381,8 +400,7 @@ mfa_status launch_weights(const CUtensorMap& mk, KeyWeightParams p, cudaStream_t
     p.ring = units(p.qtiles);
     if (p.ring > kMaxRing) p.ring = kMaxRing;
     const int bytes = p.ring * C::kUnit + p.qtiles * C::kQTile + C::rest(p.qtiles, p.T, p.words);
-    mfa_key_weights_kernel<D, NR><<<p.ctas, kThreads, bytes, s>>>(mk, p);
-    if (cudaGetLastError() != cudaSuccess) return MFA_ERR_CUDA;
+    if (!launch_after(mfa_key_weights_kernel<D, NR>, dim3(p.ctas), kThreads, bytes, s, mk, p)) return MFA_ERR_CUDA;
     // Later rows add to what this pass wrote.
     p.w_in = p.w_out;
     p.decay = 1.f;

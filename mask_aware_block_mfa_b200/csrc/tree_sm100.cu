@@ -77,7 +77,7 @@ struct Cfg {
   static constexpr int kRingK = D == 64 ? 4 : 2;
   static constexpr int kRingV = D == 64 ? 4 : (NR == 128 ? 2 : 3);
   static constexpr int kRing = kRingK + kRingV;         // K's slots first
-  static constexpr int kExtra = D == 256 ? 1 : D == 64 ? 4 : 2;  // see Line
+  static constexpr int kExtra = NR == 128 ? 6 : D == 256 ? 1 : D == 64 ? 4 : 2;  // see Line
   static constexpr int kQ = 0;                          // NR rows x 128 B per 64 columns
   static constexpr int kQBytes = NR * D * 2;
   static constexpr int kRing0 = (kQBytes + 1023) / 1024 * 1024;
@@ -183,6 +183,29 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 
   // The merging kernel may be scheduled now: it waits for this grid to end.
   asm volatile("griddepcontrol.launch_dependents;");
+  if (warp == C::kSoftWarps + 2 && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], C::kSoftWarps);
+      mbar_init(&p_full[i], C::kSoftWarps);
+      mbar_init(&p_empty[i], 2);
+      mbar_init(&drain[i], 1);
+    }
+    for (int i = 0; i < C::kGroups; ++i) {
+      mbar_init(&voted[i], 4);
+      sOver[2 * i] = sOver[2 * i + 1] = 0;
+    }
+    mbar_init(q_full, C::kSoftWarps * 32);
+    *s_abort = 0;
+    fence_mbarrier_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Line ln{p.lens, p.B, p.Hkv, p.N, last_node<NR>(p, rt), C::kExtra};
   const Start start = find_start(ln, cta, p.groups);
   if (start.b < 0) return;  // more CTAs than places
@@ -203,26 +226,29 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   constexpr bool kEarlyQ = NR < 128;  // the next pair's during the last tile (where the registers allow it)
   uint4 qy[kPer];
   if (warp < C::kSoftWarps) fetch_q(w.b, w.g, qy);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < RING; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+  const uint32_t ring = smem_u32(smem + C::kRing0);
+  // The TMA producer's state: K (and V) units issued; slots ever loaded, parity of the last load.
+  uint32_t idx = 0, used = 0, phase = 0;
+  // K and V of tile t; false when a wait ran out.
+  auto load_tile = [&](int t) {
+#pragma unroll
+    for (int x = 0; x < 2 * U; ++x) {
+      const bool isv = x >= U;
+      const uint32_t u = x % U, at = idx + u, ring_n = isv ? RV : RK;
+      const uint32_t slot = (isv ? RK : 0) + at % ring_n;
+      if (at >= ring_n && !mbar_wait(&empty[slot], (at / ring_n - 1) & 1, s_abort)) return false;
+      mbar_arrive_expect_tx(&full[slot], C::kUnit);
+      uint8_t* dst = smem + C::kRing0 + slot * C::kUnit;
+#pragma unroll
+      for (int c = 0; c < C::kUnit / kChunk; ++c)
+        tma_load_4d(dst + c * kChunk, isv ? &tm_v : &tm_k, &full[slot], u * 128 + c * 64, t * kKeys, w.g, w.b);
+      used |= 1u << slot;
+      phase = at / ring_n & 1 ? phase | 1u << slot : phase & ~(1u << slot);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], C::kSoftWarps);
-      mbar_init(&p_full[i], C::kSoftWarps);
-      mbar_init(&p_empty[i], 2);
-      mbar_init(&drain[i], 1);
-    }
-    for (int i = 0; i < C::kGroups; ++i) {
-      mbar_init(&voted[i], 4);
-      sOver[2 * i] = sOver[2 * i + 1] = 0;
-    }
-    mbar_init(q_full, C::kSoftWarps * 32);
-    *s_abort = 0;
-    fence_mbarrier_init();
-  }
+    idx += U;
+    return true;
+  };
+  if (warp == C::kSoftWarps + 2 && lane == 0) load_tile(w.t0);
   if (warp == C::kSoftWarps) {
     tmem_alloc(s_tmem, C::kTmem);
     tmem_relinquish();
@@ -231,35 +257,16 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const uint32_t ring = smem_u32(smem + C::kRing0);
 
   if (warp >= C::kSoftWarps) {
    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
    if (warp == C::kSoftWarps + 2) {
     // =================== TMA producer ===================
     if (lane == 0) {
-      uint32_t idx = 0;              // K (and V) units issued
-      uint32_t used = 0, phase = 0;  // slots: ever loaded, parity of the last load
       bool ok = true;
-      do {
-        for (int t = w.t0; t < w.t1 && ok; ++t) {
-#pragma unroll
-          for (int x = 0; x < 2 * U; ++x) {
-            const bool isv = x >= U;
-            const uint32_t u = x % U, at = idx + u, ring_n = isv ? RV : RK;
-            const uint32_t slot = (isv ? RK : 0) + at % ring_n;
-            if (at >= ring_n && !(ok = mbar_wait(&empty[slot], (at / ring_n - 1) & 1, s_abort))) break;
-            mbar_arrive_expect_tx(&full[slot], C::kUnit);
-            uint8_t* dst = smem + C::kRing0 + slot * C::kUnit;
-#pragma unroll
-            for (int c = 0; c < C::kUnit / kChunk; ++c)
-              tma_load_4d(dst + c * kChunk, isv ? &tm_v : &tm_k, &full[slot], u * 128 + c * 64, t * kKeys, w.g, w.b);
-            used |= 1u << slot;
-            phase = at / ring_n & 1 ? phase | 1u << slot : phase & ~(1u << slot);
-          }
-          idx += U;
-        }
-      } while (ok && w.next(ln));
+      for (int t = w.t0 + 1; t < w.t1 && ok; ++t) ok = load_tile(t);
+      while (ok && w.next(ln))
+        for (int t = w.t0; t < w.t1 && ok; ++t) ok = load_tile(t);
       if (*s_abort) {
         // Loads in flight land before the CTA exits.
         volatile int no_abort = 0;
@@ -695,6 +702,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
   const int rt = blockIdx.y % p.rtiles;
   const int r = SPLIT ? blockIdx.y / p.rtiles : blockIdx.y / p.rtiles * kMergeWarps + warp;  // row of the row tile
   const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
+  asm volatile("griddepcontrol.launch_dependents;");
   if (r >= min(NR, p.R - rt * NR)) return;  // (SPLIT: the whole block)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The CTAs that met the pair.
@@ -809,23 +817,14 @@ mfa_status launch_tree(const CUtensorMap& mk, const CUtensorMap& mv, const TreeP
   using C = Cfg<D, NR>;
   static std::atomic<uint64_t> attr_devs{0};
   if (!ensure_smem_attr(reinterpret_cast<const void*>(mfa_tree_kernel<D, NR>), C::kBytes, attr_devs)) return MFA_ERR_CUDA;
-  mfa_tree_kernel<D, NR><<<static_cast<unsigned>(p.rtiles) * p.groups, C::kThreads, C::kBytes, s>>>(mk, mv, p);
-  if (cudaGetLastError() != cudaSuccess) return MFA_ERR_CUDA;
+  if (!launch_after(mfa_tree_kernel<D, NR>, dim3(static_cast<unsigned>(p.rtiles) * p.groups), C::kThreads, C::kBytes, s, mk, mv, p))
+    return MFA_ERR_CUDA;
   if (p.groups > 1) {
     const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
     const int rows = p.R < NR ? p.R : NR;
     const bool split = pairs * p.R <= 1024;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>((split ? rows : cdiv64(rows, kMergeWarps)) * p.rtiles));
-    cfg.blockDim = dim3(kMergeWarps * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if ((split ? cudaLaunchKernelEx(&cfg, mfa_tree_merge<D, NR, true>, p)
-               : cudaLaunchKernelEx(&cfg, mfa_tree_merge<D, NR, false>, p)) != cudaSuccess)
+    const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>((split ? rows : cdiv64(rows, kMergeWarps)) * p.rtiles));
+    if (!launch_after(split ? mfa_tree_merge<D, NR, true> : mfa_tree_merge<D, NR, false>, grid, kMergeWarps * 32, 0, s, p))
       return MFA_ERR_CUDA;
   }
   return MFA_OK;
