@@ -99,21 +99,25 @@ __device__ __forceinline__ int places_per_cta(int total, int ctas) {
 // load and two shuffle reductions, without a block barrier): the line's length, the CTA's
 // first place, the batch that holds it (-1: past the end) and the length before that batch.
 struct Start {
-  int total, begin, before, b;
+  int total, begin, before, b, len;  // len: of batch b
 };
 __device__ __forceinline__ Start find_start(const Line& ln, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
-  Start s{0, 0, 0, -1};
-  int keep = 0;  // of batch `lane` of the last 32
+  Start s{0, 0, 0, -1, 0};
+  int keep = 0, n = 0;  // of batch `lane` of the last 32, and its length
   for (int b0 = 0; b0 < ln.B; b0 += 32) {
-    keep = b0 + lane < ln.B ? ln.tiles(ln.len(b0 + lane)) + ln.extra : 0;
+    n = b0 + lane < ln.B ? ln.len(b0 + lane) : 0;
+    keep = b0 + lane < ln.B ? ln.tiles(n) + ln.extra : 0;
     s.total += __reduce_add_sync(0xffffffffu, keep);
   }
   s.total *= ln.Hkv;
   s.begin = cta * places_per_cta(s.total, ctas);
   int done = 0;  // of the batches before
   for (int b0 = 0; b0 < ln.B && s.b < 0; b0 += 32) {
-    if (ln.B > 32) keep = b0 + lane < ln.B ? ln.tiles(ln.len(b0 + lane)) + ln.extra : 0;
+    if (ln.B > 32) {
+      n = b0 + lane < ln.B ? ln.len(b0 + lane) : 0;
+      keep = b0 + lane < ln.B ? ln.tiles(n) + ln.extra : 0;
+    }
     int sum = keep;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
@@ -124,6 +128,7 @@ __device__ __forceinline__ Start find_start(const Line& ln, int cta, int ctas) {
     if (in) {
       const int l = __ffs(in) - 1;
       s.b = b0 + l < ln.B ? b0 + l : -1;
+      s.len = __shfl_sync(0xffffffffu, n, l);
       s.before = done + __shfl_sync(0xffffffffu, sum - keep, l) * ln.Hkv;
     }
     done += __shfl_sync(0xffffffffu, sum, 31) * ln.Hkv;
@@ -140,7 +145,7 @@ struct Walk {
   __device__ __forceinline__ Walk(const Line& ln, const Start& s, int ctas) {
     left = min(places_per_cta(s.total, ctas), s.total - s.begin);
     b = s.b;
-    len = ln.len(b);
+    len = s.len;
     nt = ln.tiles(len);
     const int in = s.begin - s.before;
     g = in / (nt + ln.extra);

@@ -66,18 +66,15 @@ struct Cfg {
   static constexpr int kCols = NR < 32 ? NR : 32;       // rows (registers) per softmax thread
   static constexpr int kGroups = NR / kCols;            // groups of 4 softmax warps
   static constexpr int kSoftWarps = 4 * kGroups;
-  // With 16 softmax warps the SM's registers come to 96 per thread, of which the
-  // other warps (a fourth one is idle) give some up: 640 x 96 = 512 x 104 + 128 x 64.
-  static constexpr bool kSplitRegs = kSoftWarps == 16;
-  static constexpr int kThreads = (kSoftWarps + (kSplitRegs ? 4 : 3)) * 32;
+  static constexpr int kThreads = (kSoftWarps + 3) * 32;
   static constexpr int kUnits = D == 256 ? 2 : 1;       // ring units of a K (or V) tile
   static constexpr int kUnit = (D == 64 ? 1 : 2) * kChunk;
   static constexpr int kPBytes = (NR + 63) / 64 * kChunk;
   static constexpr int kPBufs = D == 256 && NR == 64 ? 1 : 2;
   static constexpr int kRingK = D == 64 ? 4 : 2;
-  static constexpr int kRingV = D == 64 ? 4 : (NR == 128 ? 2 : 3);
+  static constexpr int kRingV = D == 64 ? 4 : 3;
   static constexpr int kRing = kRingK + kRingV;         // K's slots first
-  static constexpr int kExtra = NR == 128 ? 6 : D == 256 ? 1 : D == 64 ? 4 : 2;  // see Line
+  static constexpr int kExtra = D == 256 ? 1 : D == 64 ? 4 : 2;  // see Line
   static constexpr int kQ = 0;                          // NR rows x 128 B per 64 columns
   static constexpr int kQBytes = NR * D * 2;
   static constexpr int kRing0 = (kQBytes + 1023) / 1024 * 1024;
@@ -86,7 +83,7 @@ struct Cfg {
   static constexpr int kBytes = kMisc + NR * 17 + 360;
   static constexpr int kO = 2 * NR;                     // TMEM columns: S0 [0, NR) S1 [NR, 2 NR) O [2 NR, (2 + kUnits) NR)
   static constexpr int kTmem = 4 * NR;
-  static_assert(D != 256 || NR <= 64, "Q and P leave no room for the ring");
+  static_assert(NR <= 64, "rows");
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(kTmem <= 512, "TMEM columns");
 };
@@ -147,6 +144,54 @@ __device__ __forceinline__ float warp_reduce_spread(float (&v)[C], int lane, Op 
     }
   }
   return v[0];
+}
+
+// By the warp that issues P.V, before tile t's: V of a key that is not before
+// the sequence's end must be finite, seen or not, as 0 * inf would reach every
+// row. Rows of V that are not, and rows past the last node, become zeros; the rows of the output
+// that see such a node become NaN in the epilogue, by the bits in bad (a tree) and *bad_min
+// (a chain). Key r's columns are 128-byte rows of 64 columns in the U ring units `unit`.
+// Returns how many steps of 16 keys the product has.
+template <int D, int U>
+__device__ __forceinline__ int clean_values(const TreeParams& p, const Walk& w, int t, int lane, uint32_t* bad, int* bad_min,
+                                            uint8_t* const (&unit)[U]) {
+  if (t == w.t0) {
+    if (lane < kSeenWords) bad[lane] = 0u;
+    if (lane == 0) *bad_min = INT_MAX;
+    __syncwarp();
+  }
+  if (t * kKeys + kKeys <= w.len) return kKeys / 16;
+  constexpr int kWide = D < 128 ? D / 8 : 16, kAtOnce = 32 / kWide;  // 16-byte units of a row in a ring unit; rows
+  const int begin = max(w.len - t * kKeys, 0), end = min(min(w.len + p.T, p.N) - t * kKeys, kKeys);
+  const int steps = (end + 15) / 16, c = lane % kWide;
+  uint8_t* mine[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) mine[u] = unit[u] + (c >> 3) * kChunk + (c & 7) * 16;
+#pragma unroll 4
+  for (int r0 = begin; r0 < steps * 16; r0 += kAtOnce) {
+    const int r = r0 + lane / kWide;
+    uint32_t x = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint4 y = r < end ? *reinterpret_cast<const uint4*>(mine[u] + r * 128) : make_uint4(0u, 0u, 0u, 0u);
+      x |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u)) |
+           (__vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u));
+    }
+    const unsigned lanes = __ballot_sync(0xffffffffu, x != 0);
+    const bool broken = (lanes >> (lane / kWide * kWide) & ((1u << (kWide - 1)) * 2u - 1u)) != 0u;
+    if (broken || (r >= end && r < steps * 16)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(mine[u] + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (broken && c == 0) {
+      const int node = t * kKeys + r - w.len;
+      if (p.parents) atomicOr(bad + (node >> 5), 1u << (node & 31));
+      atomicMin(bad_min, node);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  return steps;
 }
 
 template <int D, int NR>
@@ -259,7 +304,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   const uint32_t tmem = *s_tmem;
 
   if (warp >= C::kSoftWarps) {
-   if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
    if (warp == C::kSoftWarps + 2) {
     // =================== TMA producer ===================
     if (lane == 0) {
@@ -315,67 +359,32 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         const uint32_t first = static_cast<uint32_t>(n) * U;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_full[n % PB], (n / PB) & 1, s_abort)))) break;
         const uint32_t pb = sdesc_sw128_lo(smem_u32(smem + C::kP) + (n % PB) * C::kPBytes, kChunk);
-        if (t == w.t0) {
-          if (lane < kSeenWords) sBad[lane] = 0u;
-          if (lane == 0) *sBadMin = INT_MAX;
-          __syncwarp();
-        }
         if (t * kKeys + kKeys > w.len) {
-          // V of a key that is not before the sequence's end must be finite, seen or
-          // not: 0 * inf would reach every row. Rows that are not become zeros, and
-          // the rows of the output that see one become NaN in the epilogue.
 #pragma unroll
           for (int u = 0; u < U; ++u)
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[RK + (first + u) % RV], ((first + u) / RV) & 1, s_abort));
           if (!ok) break;
-          constexpr int kWide = D < 128 ? D / 8 : 16, kAtOnce = 32 / kWide;  // 16-byte units of a row in a ring unit; rows
-          const int begin = max(w.len - t * kKeys, 0), end = min(min(w.len + p.T, p.N) - t * kKeys, kKeys);
-          const int c = lane % kWide;
-          auto at = [&](int u, int r) {
-            return reinterpret_cast<uint4*>(smem + C::kRing0 + (RK + (first + u) % RV) * C::kUnit + (c >> 3) * kChunk + r * 128 + (c & 7) * 16);
-          };
-#pragma unroll 2
-          for (int r0 = begin; r0 < end; r0 += kAtOnce) {
-            const int r = r0 + lane / kWide;
-            uint32_t bad = 0;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const uint4 y = r < end ? *at(u, r) : make_uint4(0u, 0u, 0u, 0u);
-              bad |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u)) |
-                     (__vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u));
-            }
-            const unsigned lanes = __ballot_sync(0xffffffffu, bad != 0);
-            if (lanes >> (lane / kWide * kWide) & ((1u << (kWide - 1)) * 2u - 1u)) {
-#pragma unroll
-              for (int u = 0; u < U; ++u) *at(u, r) = make_uint4(0u, 0u, 0u, 0u);
-              if (c == 0) {
-                const int node = t * kKeys + r - w.len;
-                if (p.parents) atomicOr(sBad + (node >> 5), 1u << (node & 31));
-                atomicMin(sBadMin, node);
-              }
-            }
-          }
-#pragma unroll 4
-          for (int r0 = max(end, begin); r0 < kKeys; r0 += kAtOnce) {
-            const int r = r0 + lane / kWide;
-            if (r < kKeys) {
-#pragma unroll
-              for (int u = 0; u < U; ++u) *at(u, r) = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
         }
+        uint8_t* unit[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) unit[u] = smem + C::kRing0 + (RK + (first + u) % RV) * C::kUnit;
+        const int steps = clean_values<D, U>(p, w, t, lane, sBad, sBadMin, unit);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const uint32_t slot = RK + (first + u) % RV;
           if (!(ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[slot], ((first + u) / RV) & 1, s_abort)))) break;
           tc_fence_after();
           const uint32_t va = sdesc_sw128_lo(ring + slot * C::kUnit, kChunk);
+          const uint32_t more_o = t > w.t0 ? 1u : 0u, d_o = tmem + C::kO + u * NR;
+          if (steps == kKeys / 16) {
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            umma_ss(tmem + C::kO + u * NR, va + kk * (16 * 128 / 16), pb + kk * (16 * 128 / 16), idesc,
-                    (t > w.t0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              umma_ss(d_o, va + kk * (16 * 128 / 16), pb + kk * (16 * 128 / 16), idesc, kk > 0 ? 1u : more_o);
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk < steps; ++kk)
+              umma_ss(d_o, va + kk * (16 * 128 / 16), pb + kk * (16 * 128 / 16), idesc, kk > 0 ? 1u : more_o);
+          }
           umma_commit(&empty[slot]);
         }
         umma_commit(&p_empty[n % PB]);
@@ -387,7 +396,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     mbar_wait(&drain[1], 0, &no_abort);
    }
   } else {
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // =================== softmax and epilogue: a thread per key ===================
     // A failed wait raises *s_abort and the thread runs on (every later wait
     // then fails at once): the barriers below need all of the group's threads.
@@ -685,6 +693,409 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// More than 64 rows (D up to 128): the rows as the MMA's 128, S = Q K^T and
+// O += P V. With the keys as rows both operands of every product come from
+// shared memory, 8 KB for each 128 x 128 x 16 product of 64 cycles, which with P's
+// way through it and the loads' fills it (2,700 cycles per 128 rows and 128
+// keys measured). Here P goes through tensor memory and halves that. Two groups of 128 threads, a
+// thread per row, take turns on the tiles, each with its own S, running
+// maximum, sum and output; the two are merged when the pair ends, as parts
+// are. A group's S(n + 2) waits for its P.V(n), which has P in S's place, so the
+// groups' softmaxes and products interleave.
+// ---------------------------------------------------------------------------
+template <int D>
+struct RowCfg {
+  static constexpr int kExtra = 4;
+  static constexpr int kThreads = 384;                  // two softmax groups; MMA and TMA warps, two idle ones
+  static constexpr int kRegsLow = 96, kRegsHigh = 200;  // 384 x 168 >= 128 x 96 + 256 x 200
+  static constexpr int kTile = D / 64 * kChunk;         // K or V of a tile
+  static constexpr int kRing = D == 64 ? 5 : 3;         // tiles of each
+  static constexpr int kQ = 0;                          // 128 rows x 128 B per 64 columns
+  static constexpr int kK = kTile, kV = kK + kRing * kTile;
+  static constexpr int kMisc = kV + kRing * kTile;
+  static constexpr int kBytes = kMisc + 2 * 2 * 128 * 4 + MFA_TREE_MAX_NODES * 2 + 40 + (4 * kRing + 8) * 8 + 8;
+  static constexpr int kO = 256;                        // TMEM columns: S0 [0, 128) S1 [128, 256) O0, O1 [256, 256 + 2 D)
+  static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "register split");
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
+    mfa_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ TreeParams p) {
+  using C = RowCfg<D>;
+  constexpr int RING = C::kRing, NR = 128;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rt = blockIdx.x % p.rtiles, cta = blockIdx.x / p.rtiles;
+
+  float* sM = reinterpret_cast<float*>(smem + C::kMisc);       // [2][128] the groups' maxima and sums
+  float* sL = sM + 2 * 128;
+  int16_t* sUp = reinterpret_cast<int16_t*>(sL + 2 * 128);     // [T] a tree's parents, as tree_up gives them; -2: no node
+  uint32_t* sBad = reinterpret_cast<uint32_t*>(sUp + MFA_TREE_MAX_NODES);  // as in mfa_tree_kernel
+  int* sBadMin = reinterpret_cast<int*>(sBad + kSeenWords);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sBadMin + 2);  // [RING]
+  uint64_t* k_empty = k_full + RING;
+  uint64_t* v_full = k_empty + RING;
+  uint64_t* v_empty = v_full + RING;
+  uint64_t* q_full = v_empty + RING;
+  uint64_t* s_full = q_full + 1;   // [2]
+  uint64_t* p_full = s_full + 2;   // [2]
+  uint64_t* pv_done = p_full + 2;  // [2] a group's last P.V of a pair is done
+  uint64_t* drain = pv_done + 2;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (warp == 10 && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 2);
+    }
+    mbar_init(drain, 1);
+    mbar_init(q_full, 256);
+    *s_abort = 0;
+    fence_mbarrier_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Line ln{p.lens, p.B, p.Hkv, p.N, last_node<NR>(p, rt), C::kExtra};
+  const Start start = find_start(ln, cta, p.groups);
+  if (start.b < 0) return;  // more CTAs than places
+  Walk w(ln, start, p.groups);
+  if (!w.more) return;      // none of them a tile
+  // Q of a pair, zeros for rows that are none.
+  constexpr int kPer = NR * (D / 8) / 256, kStep = 256 / (D / 8);
+  const int qu = threadIdx.x % (D / 8), qr = threadIdx.x / (D / 8);
+  uint4 qy[kPer];
+  auto fetch_q = [&](int b, int g) {
+    const __nv_bfloat16* src = p.q + b * p.qs[0] + static_cast<int64_t>(g) * p.G * p.qs[1] + qu * 8;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int row = min(rt * NR + qr + k * kStep, p.R - 1), t = p.by_g(row), h = row - t * p.G;
+      qy[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
+    }
+  };
+  if (warp < 8) fetch_q(w.b, w.g);
+  int tiles = 0, loads_k = 0;  // the producer's: tiles loaded, K loads
+  auto load_tile = [&](int t) {
+    const int slot = tiles % RING, round = tiles / RING;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (round > 0 && !mbar_wait(x ? &v_empty[slot] : &k_empty[slot], (round - 1) & 1, s_abort)) return false;
+      uint64_t* full = x ? &v_full[slot] : &k_full[slot];
+      mbar_arrive_expect_tx(full, C::kTile);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_4d(smem + (x ? C::kV : C::kK) + slot * C::kTile + c * kChunk, x ? &tm_v : &tm_k, full, c * 64, t * kKeys, w.g, w.b);
+      if (x == 0) ++loads_k;
+    }
+    ++tiles;
+    return true;
+  };
+  if (warp == 10 && lane == 0) load_tile(w.t0);
+  if (warp == 8) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsLow));
+    if (warp == 10) {
+      // =================== TMA producer ===================
+      if (lane == 0) {
+        bool ok = true;
+        for (int t = w.t0 + 1; t < w.t1 && ok; ++t) ok = load_tile(t);
+        while (ok && w.next(ln))
+          for (int t = w.t0; t < w.t1 && ok; ++t) ok = load_tile(t);
+        if (*s_abort) {
+          // Loads in flight land before the CTA exits.
+          volatile int no_abort = 0;
+          for (int j = loads_k > RING ? loads_k - RING : 0; j < loads_k; ++j) mbar_wait(&k_full[j % RING], (j / RING) & 1, &no_abort);
+          for (int j = tiles > RING ? tiles - RING : 0; j < tiles; ++j) mbar_wait(&v_full[j % RING], (j / RING) & 1, &no_abort);
+        }
+      }
+    } else if (warp == 8) {
+      // =================== S = Q K^T, O += P V ===================
+      // P.V(n) and S(n + 2), which overwrites its P, go out together: products of one thread
+      // run in order. S of the next pair follows the pair's last P.V, as it waits for the next Q.
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, kKeys, false), idesc_o = idesc_bf16_f32(128, D, true);
+      const uint32_t q_addr = smem_u32(smem + C::kQ), k_addr = smem_u32(smem + C::kK), v_addr = smem_u32(smem + C::kV);
+      bool ok = true;
+      int n = 0, seg = 0;  // the next P.V's tile; pairs begun
+      auto issue_s = [&](int k) {
+        const int slot = k % RING;
+        if (!__all_sync(0xffffffffu, mbar_wait(&k_full[slot], (k / RING) & 1, s_abort))) return false;
+        tc_fence_after();
+        const uint32_t kb = k_addr + slot * C::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kChunk + (kk & 3) * 32;
+          umma_ss(tmem + (k & 1) * 128, sdesc_sw128_lo(q_addr + off, 16), sdesc_sw128_lo(kb + off, 16), idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[k & 1]);
+        umma_commit(&k_empty[slot]);
+        return true;
+      };
+      do {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(q_full, seg & 1, s_abort));
+        ok = ok && issue_s(n);
+        if (w.t1 - w.t0 > 1) ok = ok && issue_s(n + 1);
+        for (int t = w.t0; t < w.t1 && ok; ++t, ++n) {
+          const int slot = n % RING;
+          ok = __all_sync(0xffffffffu, mbar_wait(&v_full[slot], (n / RING) & 1, s_abort)) &&
+               __all_sync(0xffffffffu, mbar_wait(&p_full[n & 1], (n >> 1) & 1, s_abort));
+          if (!ok) break;
+          uint8_t* unit[1] = {smem + C::kV + slot * C::kTile};
+          const int steps = clean_values<D, 1>(p, w, t, lane, sBad, sBadMin, unit);
+          tc_fence_after();
+          const uint32_t vd = sdesc_sw128_lo(v_addr + slot * C::kTile, kChunk);
+          const uint32_t a_p = tmem + (n & 1) * 128, d_o = tmem + C::kO + (n & 1) * D;
+          const uint32_t more_o = t >= w.t0 + 2 ? 1u : 0u;
+          // (Unrolled for whole tiles: a step behind a condition takes twice its 64 cycles to issue.)
+          if (steps == kKeys / 16) {
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk) umma_ts(d_o, a_p + kk * 8, vd + kk * (16 * 128 / 16), idesc_o, kk > 0 ? 1u : more_o);
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk < steps; ++kk) umma_ts(d_o, a_p + kk * 8, vd + kk * (16 * 128 / 16), idesc_o, kk > 0 ? 1u : more_o);
+          }
+          umma_commit(&v_empty[slot]);
+          if (t + 2 < w.t1) {
+            ok = issue_s(n + 2);
+          } else {
+            // The group's last of the pair: its epilogue waits for it.
+            umma_commit(&pv_done[n & 1]);
+            if (lane == 0) mbar_arrive(&pv_done[n & 1]);  // (orders sBad before the epilogue)
+          }
+        }
+        ++seg;
+      } while (ok && w.next(ln));
+      umma_commit(drain);
+      volatile int no_abort = 0;
+      mbar_wait(drain, 0, &no_abort);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsHigh));
+    // =================== softmax and epilogue: a thread per row ===================
+    // (A failed wait raises *s_abort and the thread runs on, as in mfa_tree_kernel.)
+    const int grp = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane, row = rt * NR + r;  // the thread's row of the tile, of the pair
+    const bool real = row < p.R;
+    const int node = real ? p.by_g(row) : 0, head = row - node * p.G;
+    const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    auto store_q = [&]() {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int x = qr + k * kStep;
+        if (rt * NR + x >= p.R) qy[k] = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(smem + C::kQ + (qu >> 3) * kChunk + x * 128 + (((qu & 7) ^ (x & 7)) << 4)) = qy[k];
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+    };
+    store_q();
+    int n = 0;  // tiles of the CTA before the pair's first
+    uint32_t lasts = 0;  // of the group's last P.V of a pair
+    do {
+      const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
+      if (par) {
+        for (int i = threadIdx.x; i < p.T; i += 256) sUp[i] = static_cast<int16_t>(__ldg(par + i) == -2 ? -2 : tree_up(par, i));
+      }
+      if (rt == 0 && w.g == 0 && w.t0 == 0) {
+        for (int t = threadIdx.x; t < (par ? p.T : 1); t += 256) {
+          const uint32_t e = draft_errors(p.lens, p.parents, w.b, t, p.T, p.N);
+          if (e) atomicOr(p.err, e);
+        }
+      }
+      if (par) named_barrier(1, 256);
+      const bool dead = par && sUp[node] == -2;
+      float m = -INFINITY, l = 0.f;
+      const int count = w.t1 - w.t0;
+      for (int i = (n & 1) == grp ? 0 : 1; i < count; i += 2) {
+        const int k = n + i, base = (w.t0 + i) * kKeys;  // the tile's number in the CTA, its first key
+        mbar_wait(&s_full[grp], (k >> 1) & 1, s_abort);
+        tc_fence_after();
+        float x[kKeys];
+        {
+          uint32_t y[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tm + grp * 128 + c * 32, y[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) x[c] = __uint_as_float(y[c >> 5][c & 31]);
+        }
+        if (base + kKeys > w.len) {
+          // ---- a tile with drafted keys, or the last: the keys the row sees, as bits ----
+          const int own = w.len - base;  // drafted keys begin here
+          uint32_t see[4];
+          if (!par) {
+            const int hi = min(own + node, p.N - 1 - base);  // the last one seen
+#pragma unroll
+            for (int c = 0; c < 4; ++c) see[c] = ~rows_from(hi + 1 - c * 32);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) see[c] = ~rows_from(own - c * 32);
+            for (int a = dead ? -1 : node; a >= 0; a = sUp[a]) {
+              const int at = own + a;
+              if (at < p.N - base) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) see[c] |= (at >> 5) == c ? 1u << (at & 31) : 0u;
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            if (!(see[c >> 5] >> (c & 31) & 1)) x[c] = -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 8) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mx[y] = fmax3(mx[y], x[c + 2 * y], x[c + 2 * y + 1]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const bool need = top > m + kLazy;
+        const float m_new = need ? top : m, m_use = m_new == -INFINITY ? 0.f : m_new;
+        if (i >= 2 && __any_sync(0xffffffffu, need)) {
+          // Rare: the row's sums so far shrink. O holds every P.V of the group before
+          // this tile's: S(k) went out after P.V(k - 2).
+          const float alpha = need ? ex2_approx(m - m_use) : 1.f;  // (m = -inf: 0, and the sums are 0)
+          l *= alpha;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tm + C::kO + grp * D + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+            tmem_st_32x32b_x32(tm + C::kO + grp * D + c, o);
+          }
+        }
+        m = m_new;
+        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(-m_use, -m_use);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float a, b;
+            f2_unpack(f2_fma(f2_pack(x[h * 64 + 2 * c], x[h * 64 + 2 * c + 1]), sc2, nm2), a, b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            sum[c & 1] = f2_add(sum[c & 1], f2_pack(a, b));
+            pk[c] = pack_bf16x2(a, b);
+          }
+          tmem_st_32x32b_x32(tm + grp * 128 + h * 32, pk);
+        }
+        float a, b;
+        f2_unpack(f2_add(sum[0], sum[1]), a, b);
+        l += a + b;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[grp]);
+      }
+      // Q of the next pair once every S of this one is done: this group's last, and by the
+      // barrier below the other's.
+      Walk nx = w;
+      const bool more = nx.next(ln);
+      if (more) fetch_q(nx.b, nx.g);
+
+      // ---- epilogue of the pair: merge the groups ----
+      const int end = n + count;
+      if (count > ((n & 1) == grp ? 0 : 1)) {  // the group had a tile
+        mbar_wait(&pv_done[grp], lasts & 1, s_abort);
+        ++lasts;
+        tc_fence_after();
+      }
+      sM[grp * 128 + r] = m;
+      sL[grp * 128 + r] = l;
+      named_barrier(1, 256);
+      tc_fence_after();
+      if (more) store_q();
+      {
+        const float m0 = sM[r], m1 = sM[128 + r], l0 = sL[r], l1 = sL[128 + r];
+        const float M = fmaxf(m0, m1);  // (-inf: no key seen, or only NaN scores)
+        const float M_use = M == -INFINITY ? 0.f : M;
+        const float f0 = m0 == -INFINITY ? 1.f : ex2_approx(m0 - M_use), f1 = m1 == -INFINITY ? 1.f : ex2_approx(m1 - M_use);
+        const bool has0 = l0 != 0.f, has1 = l1 != 0.f;  // (a group without one may hold anything in O)
+        const float sum = dead ? 0.f : (has0 ? l0 * f0 : 0.f) + (has1 ? l1 * f1 : 0.f);
+        const bool whole = w.t0 == 0 && w.t1 == w.nt, any = real && sum != 0.f;
+        bool poison = *sBadMin <= node;
+        if (poison && par) {
+          poison = false;
+          for (int x = node; x >= 0; x = sUp[x]) poison |= sBad[x >> 5] >> (x & 31) & 1u;
+        }
+        const float g = poison ? NAN : whole ? 1.f / sum : 1.f;
+        const float g0 = f0 * g, g1 = f1 * g;
+        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * NR + r;
+        const int h = w.g * p.G + head;
+        if (real && grp == 0) {
+          if (whole)
+            p.lse[(static_cast<int64_t>(w.b) * p.Hq + h) * p.T + node] = any ? (M_use + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+          else
+            *reinterpret_cast<float2*>(p.ml_part + part * 2) = make_float2(any ? M_use : -FLT_MAX, sum);
+        }
+        // Group g writes columns [g D / 2, (g + 1) D / 2).
+        __nv_bfloat16* to = p.out + w.b * p.os[0] + h * p.os[1] + node * p.os[2];
+        float* part_to = p.o_part + part * D;
+#pragma unroll 1
+        for (int c = grp * (D / 2); c < (grp + 1) * (D / 2); c += 16) {
+          uint32_t o0[16], o1[16];
+          tmem_ld_32x32b_x16(tm + C::kO + c, o0);
+          tmem_ld_32x32b_x16(tm + C::kO + D + c, o1);
+          tmem_ld_wait();
+          float y[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            y[u] = has0 ? __uint_as_float(o0[u]) * g0 : 0.f;
+            if (has1) y[u] = fmaf(__uint_as_float(o1[u]), g1, y[u]);
+            if (!any) y[u] = 0.f;
+          }
+          if (real) {
+            if (whole) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                reinterpret_cast<uint4*>(to + c)[u] = make_uint4(pack_bf16x2(y[8 * u], y[8 * u + 1]), pack_bf16x2(y[8 * u + 2], y[8 * u + 3]),
+                                                                 pack_bf16x2(y[8 * u + 4], y[8 * u + 5]), pack_bf16x2(y[8 * u + 6], y[8 * u + 7]));
+            } else {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                reinterpret_cast<float4*>(part_to + c)[u] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      named_barrier(1, 256);  // O, sM, sL, sUp have been read
+      n = end;
+      w = nx;
+      if (!more) break;
+    } while (true);
+    if (*s_abort && threadIdx.x == 0) atomicOr(p.err, MFA_DEVERR_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Merges the parts of every pair that was cut: with M = max m_s, out = sum o_s
 // 2^(m_s - M) / sum l_s 2^(m_s - M). A part without a visible key has
 // m = -FLT_MAX, l = 0, o = 0 (never -inf - -inf); all such: out = 0, lse = -inf.
@@ -694,7 +1105,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
 
-template <int D, int NR, bool SPLIT>
+template <int D, int NR, int EXTRA, bool SPLIT>
 __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_constant__ TreeParams p) {
   constexpr int E = D / 32, WS = SPLIT ? kMergeWarps : 1;
   __shared__ float so[SPLIT ? kMergeWarps : 1][D];
@@ -706,7 +1117,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
   if (r >= min(NR, p.R - rt * NR)) return;  // (SPLIT: the whole block)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The CTAs that met the pair.
-  const Line ln{p.lens, p.B, p.Hkv, p.N, last_node<NR>(p, rt), Cfg<D, NR>::kExtra};
+  const Line ln{p.lens, p.B, p.Hkv, p.N, last_node<NR>(p, rt), EXTRA};
   int before = 0, total = 0;
   for (int x = lane; x < p.B; x += 32) {
     const int n = ln.tiles(ln.len(x)) + ln.extra;
@@ -812,33 +1223,45 @@ size_t part_bytes(const TreePlan& pl, int64_t D, size_t* o_bytes) {
   return *o_bytes + align256(rows * 2 * 4) + 256;
 }
 
-template <int D, int NR>
-mfa_status launch_tree(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
-  using C = Cfg<D, NR>;
-  static std::atomic<uint64_t> attr_devs{0};
-  if (!ensure_smem_attr(reinterpret_cast<const void*>(mfa_tree_kernel<D, NR>), C::kBytes, attr_devs)) return MFA_ERR_CUDA;
-  if (!launch_after(mfa_tree_kernel<D, NR>, dim3(static_cast<unsigned>(p.rtiles) * p.groups), C::kThreads, C::kBytes, s, mk, mv, p))
-    return MFA_ERR_CUDA;
+template <int D, int NR, int EXTRA, typename K>
+mfa_status launch_tree(K kernel, int threads, int bytes, std::atomic<uint64_t>& attr_devs, const CUtensorMap& mk, const CUtensorMap& mv,
+                       const TreeParams& p, cudaStream_t s) {
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), bytes, attr_devs)) return MFA_ERR_CUDA;
+  if (!launch_after(kernel, dim3(static_cast<unsigned>(p.rtiles) * p.groups), threads, bytes, s, mk, mv, p)) return MFA_ERR_CUDA;
   if (p.groups > 1) {
     const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
     const int rows = p.R < NR ? p.R : NR;
     const bool split = pairs * p.R <= 1024;
     const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>((split ? rows : cdiv64(rows, kMergeWarps)) * p.rtiles));
-    if (!launch_after(split ? mfa_tree_merge<D, NR, true> : mfa_tree_merge<D, NR, false>, grid, kMergeWarps * 32, 0, s, p))
+    if (!launch_after(split ? mfa_tree_merge<D, NR, EXTRA, true> : mfa_tree_merge<D, NR, EXTRA, false>, grid, kMergeWarps * 32, 0, s, p))
       return MFA_ERR_CUDA;
   }
   return MFA_OK;
 }
 
+template <int D, int NR>
+mfa_status launch_keys(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
+  using C = Cfg<D, NR>;
+  static std::atomic<uint64_t> attr_devs{0};
+  return launch_tree<D, NR, C::kExtra>(mfa_tree_kernel<D, NR>, C::kThreads, C::kBytes, attr_devs, mk, mv, p, s);
+}
+
+template <int D>
+mfa_status launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
+  using C = RowCfg<D>;
+  static std::atomic<uint64_t> attr_devs{0};
+  return launch_tree<D, 128, C::kExtra>(mfa_tree_rows_kernel<D>, C::kThreads, C::kBytes, attr_devs, mk, mv, p, s);
+}
+
 template <int D>
 mfa_status launch_tree_rows(int nr, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
   switch (nr) {
-    case 16: return launch_tree<D, 16>(mk, mv, p, s);
-    case 32: return launch_tree<D, 32>(mk, mv, p, s);
-    case 64: return launch_tree<D, 64>(mk, mv, p, s);
+    case 16: return launch_keys<D, 16>(mk, mv, p, s);
+    case 32: return launch_keys<D, 32>(mk, mv, p, s);
+    case 64: return launch_keys<D, 64>(mk, mv, p, s);
     default:
       if constexpr (D == 256) return MFA_ERR_UNSUPPORTED;  // plan_tree gives no such tile
-      else return launch_tree<D, 128>(mk, mv, p, s);
+      else return launch_rows<D>(mk, mv, p, s);
   }
 }
 
