@@ -19,7 +19,8 @@ __device__ __forceinline__ int cache_len(const int32_t* lens, int b, int N) {
 
 // The parent of node t (par: the batch's parents), with everything that ends
 // the way up as -1: the root, an entry outside [-2, t), a padding row.
-__device__ __forceinline__ int tree_up(const int32_t* par, int t) {
+template <typename T>
+__device__ __forceinline__ int tree_up(const T* par, int t) {
   const int p = par[t];
   return (p < 0 || p >= t) ? -1 : (par[p] == -2 ? -1 : p);
 }

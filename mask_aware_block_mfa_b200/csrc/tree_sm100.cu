@@ -174,9 +174,11 @@ __device__ __forceinline__ int clean_values(const TreeParams& p, const Walk& w, 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint4 y = r < end ? *reinterpret_cast<const uint4*>(mine[u] + r * 128) : make_uint4(0u, 0u, 0u, 0u);
-      x |= (__vcmpeq2(y.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.y & 0x7f807f80u, 0x7f807f80u)) |
-           (__vcmpeq2(y.z & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(y.w & 0x7f807f80u, 0x7f807f80u));
+      // An exponent of ones carries into the sign's place.
+      x |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) | ((y.z & 0x7f807f80u) + 0x00800080u) |
+           ((y.w & 0x7f807f80u) + 0x00800080u);
     }
+    x &= 0x80008000u;
     const unsigned lanes = __ballot_sync(0xffffffffu, x != 0);
     const bool broken = (lanes >> (lane / kWide * kWide) & ((1u << (kWide - 1)) * 2u - 1u)) != 0u;
     if (broken || (r >= end && r < steps * 16)) {
@@ -705,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 // ---------------------------------------------------------------------------
 template <int D>
 struct RowCfg {
-  static constexpr int kExtra = 4;
+  static constexpr int kExtra = 10;  // (2 to 14 measured over 12 cases of 96 to 496 rows: within 3% from 7 on)
   static constexpr int kThreads = 384;                  // two softmax groups; MMA and TMA warps, two idle ones
   static constexpr int kRegsLow = 96, kRegsHigh = 200;  // 384 x 168 >= 128 x 96 + 256 x 200
   static constexpr int kTile = D / 64 * kChunk;         // K or V of a tile
@@ -731,8 +733,8 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
 
   float* sM = reinterpret_cast<float*>(smem + C::kMisc);       // [2][128] the groups' maxima and sums
   float* sL = sM + 2 * 128;
-  int16_t* sUp = reinterpret_cast<int16_t*>(sL + 2 * 128);     // [T] a tree's parents, as tree_up gives them; -2: no node
-  uint32_t* sBad = reinterpret_cast<uint32_t*>(sUp + MFA_TREE_MAX_NODES);  // as in mfa_tree_kernel
+  int16_t* sPar = reinterpret_cast<int16_t*>(sL + 2 * 128);    // [T] a tree's parents (those past int16 as -3: they end the way up)
+  uint32_t* sBad = reinterpret_cast<uint32_t*>(sPar + MFA_TREE_MAX_NODES);  // as in mfa_tree_kernel
   int* sBadMin = reinterpret_cast<int*>(sBad + kSeenWords);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sBadMin + 2);  // [RING]
   uint64_t* k_empty = k_full + RING;
@@ -784,7 +786,14 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
       qy[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
     }
   };
-  if (warp < 8) fetch_q(w.b, w.g);
+  int parent = 0;  // of node threadIdx.x
+  auto fetch_parent = [&](int b) {
+    if (p.parents && static_cast<int>(threadIdx.x) < p.T) parent = __ldg(p.parents + static_cast<int64_t>(b) * p.T + threadIdx.x);
+  };
+  if (warp < 8) {
+    fetch_parent(w.b);
+    fetch_q(w.b, w.g);
+  }
   int tiles = 0, loads_k = 0;  // the producer's: tiles loaded, K loads
   auto load_tile = [&](int t) {
     const int slot = tiles % RING, round = tiles / RING;
@@ -855,11 +864,13 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
         if (w.t1 - w.t0 > 1) ok = ok && issue_s(n + 1);
         for (int t = w.t0; t < w.t1 && ok; ++t, ++n) {
           const int slot = n % RING;
-          ok = __all_sync(0xffffffffu, mbar_wait(&v_full[slot], (n / RING) & 1, s_abort)) &&
-               __all_sync(0xffffffffu, mbar_wait(&p_full[n & 1], (n >> 1) & 1, s_abort));
+          // (A pair's first P also says that the last epilogue has read sBad.)
+          ok = __all_sync(0xffffffffu, mbar_wait(&v_full[slot], (n / RING) & 1, s_abort));
+          if (t == w.t0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&p_full[n & 1], (n >> 1) & 1, s_abort));
           if (!ok) break;
           uint8_t* unit[1] = {smem + C::kV + slot * C::kTile};
           const int steps = clean_values<D, 1>(p, w, t, lane, sBad, sBadMin, unit);
+          if (t != w.t0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&p_full[n & 1], (n >> 1) & 1, s_abort)))) break;
           tc_fence_after();
           const uint32_t vd = sdesc_sw128_lo(v_addr + slot * C::kTile, kChunk);
           const uint32_t a_p = tmem + (n & 1) * 128, d_o = tmem + C::kO + (n & 1) * D;
@@ -911,9 +922,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
     uint32_t lasts = 0;  // of the group's last P.V of a pair
     do {
       const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
-      if (par) {
-        for (int i = threadIdx.x; i < p.T; i += 256) sUp[i] = static_cast<int16_t>(__ldg(par + i) == -2 ? -2 : tree_up(par, i));
-      }
+      if (par) sPar[threadIdx.x] = static_cast<int16_t>(parent < -2 || parent > INT16_MAX ? -3 : parent);
       if (rt == 0 && w.g == 0 && w.t0 == 0) {
         for (int t = threadIdx.x; t < (par ? p.T : 1); t += 256) {
           const uint32_t e = draft_errors(p.lens, p.parents, w.b, t, p.T, p.N);
@@ -921,7 +930,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
         }
       }
       if (par) named_barrier(1, 256);
-      const bool dead = par && sUp[node] == -2;
+      const bool dead = par && sPar[node] == -2;
       float m = -INFINITY, l = 0.f;
       const int count = w.t1 - w.t0;
       for (int i = (n & 1) == grp ? 0 : 1; i < count; i += 2) {
@@ -948,7 +957,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) see[c] = ~rows_from(own - c * 32);
-            for (int a = dead ? -1 : node; a >= 0; a = sUp[a]) {
+            for (int a = dead ? -1 : node; a >= 0; a = tree_up(sPar, a)) {
               const int at = own + a;
               if (at < p.N - base) {
 #pragma unroll
@@ -1013,7 +1022,10 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
       // barrier below the other's.
       Walk nx = w;
       const bool more = nx.next(ln);
-      if (more) fetch_q(nx.b, nx.g);
+      if (more) {
+        fetch_parent(nx.b);
+        fetch_q(nx.b, nx.g);
+      }
 
       // ---- epilogue of the pair: merge the groups ----
       const int end = n + count;
@@ -1038,7 +1050,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
         bool poison = *sBadMin <= node;
         if (poison && par) {
           poison = false;
-          for (int x = node; x >= 0; x = sUp[x]) poison |= sBad[x >> 5] >> (x & 31) & 1u;
+          for (int x = node; x >= 0; x = tree_up(sPar, x)) poison |= sBad[x >> 5] >> (x & 31) & 1u;
         }
         const float g = poison ? NAN : whole ? 1.f / sum : 1.f;
         const float g0 = f0 * g, g1 = f1 * g;
@@ -1081,7 +1093,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
         }
       }
       tc_fence_before();
-      named_barrier(1, 256);  // O, sM, sL, sUp have been read
+      named_barrier(1, 256);  // O, sM, sL, sPar have been read
       n = end;
       w = nx;
       if (!more) break;
