@@ -42,18 +42,41 @@ struct TreeParams {
   int32_t B, Hq, Hkv, G, T, N, R;  // R = T * G rows per key/value head
   FastDiv by_g;
   int32_t rtiles, groups;          // row tiles; CTAs per row tile
+  int32_t tile_t, parts;           // nodes per row tile; row tiles per node (1 unless G exceeds a tile)
   float scale_log2;
-  const __nv_bfloat16* q;
-  int64_t qs[3], os[3];
+  int64_t os[3];
   const int32_t *lens, *parents;
   __nv_bfloat16* out;
   float *lse, *o_part, *ml_part;  // parts: [rtiles * groups][2][NR][D] and [..][NR][2] (m, l)
   uint32_t* err;
 };
 
-template <int NR>
-__device__ __forceinline__ int last_node(const TreeParams& p, int rt) {
-  return min(p.by_g(rt * NR + NR - 1), p.T - 1);
+// Row tile rt: whole nodes, so that Q comes by TMA (a box of the group's heads by
+// tile_t nodes), or part of one node's heads. Rows past the last one in Q's
+// tile are zeros or other rows of Q.
+struct RowTile {
+  int row0, rows, node0, head0;  // first row, rows, first node and head
+  __device__ __forceinline__ RowTile(const TreeParams& p, int rt, int nr) {
+    if (p.parts == 1) {
+      node0 = rt * p.tile_t;
+      head0 = 0;
+      rows = min(p.tile_t, p.T - node0) * p.G;
+    } else {
+      node0 = rt / p.parts;
+      head0 = rt % p.parts * nr;
+      rows = min(nr, p.G - head0);
+    }
+    row0 = node0 * p.G + head0;
+  }
+  __device__ __forceinline__ int last_node(const TreeParams& p) const { return p.parts == 1 ? min(node0 + p.tile_t, p.T) - 1 : node0; }
+};
+
+// Q of a row tile by TMA: its boxes of 64 columns.
+template <int D, int NR>
+__device__ __forceinline__ void load_q(const TreeParams& p, const CUtensorMap* tm_q, uint8_t* to, uint64_t* full, const RowTile& rows, int b, int g) {
+  mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.parts == 1 ? p.tile_t * p.G : NR) * 128u * (D / 64));
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) tma_load_4d(to + c * (NR * 128), tm_q, full, c * 64, g * p.G + rows.head0, rows.node0, b);
 }
 
 // ---------------------------------------------------------------------------
@@ -66,7 +89,7 @@ struct Cfg {
   static constexpr int kCols = NR < 32 ? NR : 32;       // rows (registers) per softmax thread
   static constexpr int kGroups = NR / kCols;            // groups of 4 softmax warps
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kThreads = (kSoftWarps + 3) * 32;
+  static constexpr int kThreads = (kSoftWarps + 4) * 32;  // + S, P.V, TMA of K and V, TMA of Q
   static constexpr int kUnits = D == 256 ? 2 : 1;       // ring units of a K (or V) tile
   static constexpr int kUnit = (D == 64 ? 1 : 2) * kChunk;
   static constexpr int kPBytes = (NR + 63) / 64 * kChunk;
@@ -198,8 +221,8 @@ __device__ __forceinline__ int clean_values(const TreeParams& p, const Walk& w, 
 
 template <int D, int NR>
 __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
-    mfa_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const __grid_constant__ TreeParams p) {
+    mfa_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
   using C = Cfg<D, NR>;
   constexpr int U = C::kUnits, RK = C::kRingK, RV = C::kRingV, RING = C::kRing, PB = C::kPBufs, W = C::kCols;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -217,7 +240,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   uint64_t* full = bars;               // [RING]
   uint64_t* empty = full + RING;       // [RING]
   uint64_t* q_full = empty + RING;     // Q of the next pair is in shared memory
-  uint64_t* s_full = q_full + 1;       // [2]
+  uint64_t* q_empty = q_full + 1;      // the pair's S are done
+  uint64_t* s_full = q_empty + 1;      // [2]
   uint64_t* s_empty = s_full + 2;      // [2] read for the last time
   uint64_t* p_full = s_empty + 2;      // [PB]
   uint64_t* p_empty = p_full + 2;      // [PB] P.V done
@@ -226,11 +250,12 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   int* sOver = reinterpret_cast<int*>(voted + 4);  // [groups][2] tile number + 1 whose scores exceed a maximum by kLazy
   volatile int* s_abort = reinterpret_cast<volatile int*>(sOver + 8);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
-  static_assert(40 + (2 * RING + 15) * 8 + 40 <= 360, "misc");
+  static_assert(40 + (2 * RING + 16) * 8 + 40 <= 360, "misc");
 
   // The merging kernel may be scheduled now: it waits for this grid to end.
   asm volatile("griddepcontrol.launch_dependents;");
   if (warp == C::kSoftWarps + 2 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     for (int i = 0; i < RING; ++i) {
@@ -248,32 +273,20 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       mbar_init(&voted[i], 4);
       sOver[2 * i] = sOver[2 * i + 1] = 0;
     }
-    mbar_init(q_full, C::kSoftWarps * 32);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     *s_abort = 0;
     fence_mbarrier_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Line ln{p.lens, p.B, p.Hkv, p.N, last_node<NR>(p, rt), C::kExtra};
+  const RowTile tile(p, rt, NR);
+  const Line ln{p.lens, p.B, p.Hkv, p.N, tile.last_node(p), C::kExtra};
   const Start start = find_start(ln, cta, p.groups);
   if (start.b < 0) return;  // more CTAs than places
   Walk w(ln, start, p.groups);
   if (!w.more) return;      // none of them a tile
-  // Q of a pair, zeros for rows that are none. (A padding row's Q may be
-  // anything: it reaches no other row.)
-  constexpr int kPer = NR * (D / 8) / (C::kSoftWarps * 32), kStep = C::kSoftWarps * 32 / (D / 8);
-  const int qu = threadIdx.x % (D / 8), qr = threadIdx.x / (D / 8);
-  auto fetch_q = [&](int b, int g, uint4 (&y)[kPer]) {
-    const __nv_bfloat16* src = p.q + b * p.qs[0] + static_cast<int64_t>(g) * p.G * p.qs[1] + qu * 8;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int row = min(rt * NR + qr + k * kStep, p.R - 1), t = p.by_g(row), h = row - t * p.G;
-      y[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
-    }
-  };
-  constexpr bool kEarlyQ = NR < 128;  // the next pair's during the last tile (where the registers allow it)
-  uint4 qy[kPer];
-  if (warp < C::kSoftWarps) fetch_q(w.b, w.g, qy);
   const uint32_t ring = smem_u32(smem + C::kRing0);
+  const int tile_fill = p.parts == 1 ? p.tile_t * p.G : NR;  // rows of Q's box
   // The TMA producer's state: K (and V) units issued; slots ever loaded, parity of the last load.
   uint32_t idx = 0, used = 0, phase = 0;
   // K and V of tile t; false when a wait ran out.
@@ -295,7 +308,14 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     idx += U;
     return true;
   };
-  if (warp == C::kSoftWarps + 2 && lane == 0) load_tile(w.t0);
+  if (warp == C::kSoftWarps + 2 && lane == 0) {
+    load_q<D, NR>(p, &tm_q, smem + C::kQ, q_full, tile, w.b, w.g);
+    load_tile(w.t0);
+  }
+  // Rows of Q's buffer that no load fills.
+  for (int i = threadIdx.x; i < (NR - tile_fill) * (D / 8); i += C::kThreads)
+    *reinterpret_cast<uint4*>(smem + C::kQ + (i % (D / 8) >> 3) * (NR * 128) + (tile_fill + i / (D / 8)) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   if (warp == C::kSoftWarps) {
     tmem_alloc(s_tmem, C::kTmem);
     tmem_relinquish();
@@ -318,6 +338,19 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         volatile int no_abort = 0;
         for (int i = 0; i < RING; ++i)
           if (used >> i & 1) mbar_wait(&full[i], phase >> i & 1, &no_abort);
+      }
+    }
+   } else if (warp == C::kSoftWarps + 3) {
+    // =================== TMA of the next pairs' Q ===================
+    if (lane == 0) {
+      int seg = 0;  // of the last load
+      while (w.next(ln) && mbar_wait(q_empty, seg & 1, s_abort)) {
+        load_q<D, NR>(p, &tm_q, smem + C::kQ, q_full, tile, w.b, w.g);
+        ++seg;
+      }
+      if (*s_abort) {
+        volatile int no_abort = 0;
+        mbar_wait(q_full, seg & 1, &no_abort);
       }
     }
    } else if (warp == C::kSoftWarps) {
@@ -346,6 +379,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         }
         umma_commit(&s_full[n & 1]);
       }
+      umma_commit(q_empty);
       ++seg;
     } while (ok && w.next(ln));
     umma_commit(&drain[0]);
@@ -407,28 +441,16 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     constexpr uint32_t kAll = 1 + C::kGroups;   // all groups'
     const int col0 = grp * W;                   // its first row of the tile
     const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
-    const int row0 = rt * NR + col0;            // its first row of the pair
-    const int rows = min(W, p.R - row0);        // real ones (may be <= 0)
+    const int row0 = tile.row0 + col0;          // its first row of the pair
+    const int rows = min(W, tile.rows - col0);  // real ones (may be <= 0)
     float* negM = sNegM + col0;
     float* delta = sDelta + col0;
     float* alpha = sAlpha + col0;
     // Row col0 + c's slot of warp `quad` (1 to 3).
     float* slot = (quad == 1 ? sRed : quad == 2 ? sDelta : sAlpha) + col0;
     const float* red = sRed + col0;
-    auto store_q = [&](uint4 (&y)[kPer]) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int r = qr + k * kStep;
-        if (rt * NR + r >= p.R) y[k] = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(smem + C::kQ + (qu >> 3) * (NR * 128) + r * 128 + (((qu & 7) ^ (r & 7)) << 4)) = y[k];
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(q_full);
-    };
-    store_q(qy);
     int n = 0;
     uint32_t votes = 0;
-    bool more = false;
     do {
       const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
       if (tid < W) {
@@ -446,12 +468,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 #pragma unroll
       for (int c = 0; c < W / 2; ++c) l[c] = 0ull;
 
-      Walk nx = w;
-      if (kEarlyQ) more = nx.next(ln);
       for (int t = w.t0; t < w.t1; ++t, ++n) {
         const int base = t * kKeys;
         const uint32_t st = tm + (n & 1) * NR;  // the scores
-        if (kEarlyQ && more && t == w.t1 - 1) fetch_q(nx.b, nx.g, qy);
         uint8_t* pbuf = smem + C::kP + (n % PB) * C::kPBytes;
         mbar_wait(&s_full[n & 1], (n >> 1) & 1, s_abort);
         tc_fence_after();
@@ -600,16 +619,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         }
       }
 
-      // Q of the next pair now: every S of this one is done.
-      if (!kEarlyQ) {
-        nx = w;
-        more = nx.next(ln);
-      }
-      if (more) {
-        if (!kEarlyQ) fetch_q(nx.b, nx.g, qy);
-        store_q(qy);
-      }
-
       // ---- epilogue of the pair: its output, or this CTA's part of it ----
       const bool whole = w.t0 == 0 && w.t1 == w.nt;
       const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * NR + col0;
@@ -683,8 +692,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       }
       tc_fence_before();
       named_barrier(bar, 128);  // what the next pair overwrites has been read
-      w = nx;
-    } while (more);
+    } while (w.next(ln));
     if (*s_abort && threadIdx.x == 0) atomicOr(p.err, MFA_DEVERR_TIMEOUT);
   }
   __syncthreads();
@@ -708,14 +716,14 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 template <int D>
 struct RowCfg {
   static constexpr int kExtra = 10;  // (2 to 14 measured over 12 cases of 96 to 496 rows: within 3% from 7 on)
-  static constexpr int kThreads = 384;                  // two softmax groups; MMA and TMA warps, two idle ones
+  static constexpr int kThreads = 384;                  // two softmax groups; MMA, TMA of K and V, TMA of Q, an idle one
   static constexpr int kRegsLow = 96, kRegsHigh = 200;  // 384 x 168 >= 128 x 96 + 256 x 200
   static constexpr int kTile = D / 64 * kChunk;         // K or V of a tile
   static constexpr int kRing = D == 64 ? 5 : 3;         // tiles of each
   static constexpr int kQ = 0;                          // 128 rows x 128 B per 64 columns
   static constexpr int kK = kTile, kV = kK + kRing * kTile;
   static constexpr int kMisc = kV + kRing * kTile;
-  static constexpr int kBytes = kMisc + 2 * 2 * 128 * 4 + MFA_TREE_MAX_NODES * 2 + 40 + (4 * kRing + 8) * 8 + 8;
+  static constexpr int kBytes = kMisc + 2 * 2 * 128 * 4 + MFA_TREE_MAX_NODES * 2 + 40 + (4 * kRing + 9) * 8 + 8;
   static constexpr int kO = 256;                        // TMEM columns: S0 [0, 128) S1 [128, 256) O0, O1 [256, 256 + 2 D)
   static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "register split");
   static_assert(kBytes <= 232448, "shared memory");
@@ -723,8 +731,8 @@ struct RowCfg {
 
 template <int D>
 __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
-    mfa_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ TreeParams p) {
+    mfa_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
   using C = RowCfg<D>;
   constexpr int RING = C::kRing, NR = 128;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -741,7 +749,8 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
   uint64_t* v_full = k_empty + RING;
   uint64_t* v_empty = v_full + RING;
   uint64_t* q_full = v_empty + RING;
-  uint64_t* s_full = q_full + 1;   // [2]
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;  // [2]
   uint64_t* p_full = s_full + 2;   // [2]
   uint64_t* pv_done = p_full + 2;  // [2] a group's last P.V of a pair is done
   uint64_t* drain = pv_done + 2;
@@ -750,6 +759,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (warp == 10 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     for (int i = 0; i < RING; ++i) {
@@ -764,36 +774,23 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
       mbar_init(&pv_done[i], 2);
     }
     mbar_init(drain, 1);
-    mbar_init(q_full, 256);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     *s_abort = 0;
     fence_mbarrier_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Line ln{p.lens, p.B, p.Hkv, p.N, last_node<NR>(p, rt), C::kExtra};
+  const RowTile tile(p, rt, NR);
+  const Line ln{p.lens, p.B, p.Hkv, p.N, tile.last_node(p), C::kExtra};
   const Start start = find_start(ln, cta, p.groups);
   if (start.b < 0) return;  // more CTAs than places
   Walk w(ln, start, p.groups);
   if (!w.more) return;      // none of them a tile
-  // Q of a pair, zeros for rows that are none.
-  constexpr int kPer = NR * (D / 8) / 256, kStep = 256 / (D / 8);
-  const int qu = threadIdx.x % (D / 8), qr = threadIdx.x / (D / 8);
-  uint4 qy[kPer];
-  auto fetch_q = [&](int b, int g) {
-    const __nv_bfloat16* src = p.q + b * p.qs[0] + static_cast<int64_t>(g) * p.G * p.qs[1] + qu * 8;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int row = min(rt * NR + qr + k * kStep, p.R - 1), t = p.by_g(row), h = row - t * p.G;
-      qy[k] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
-    }
-  };
   int parent = 0;  // of node threadIdx.x
   auto fetch_parent = [&](int b) {
     if (p.parents && static_cast<int>(threadIdx.x) < p.T) parent = __ldg(p.parents + static_cast<int64_t>(b) * p.T + threadIdx.x);
   };
-  if (warp < 8) {
-    fetch_parent(w.b);
-    fetch_q(w.b, w.g);
-  }
+  if (warp < 8) fetch_parent(w.b);
   int tiles = 0, loads_k = 0;  // the producer's: tiles loaded, K loads
   auto load_tile = [&](int t) {
     const int slot = tiles % RING, round = tiles / RING;
@@ -810,7 +807,15 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
     ++tiles;
     return true;
   };
-  if (warp == 10 && lane == 0) load_tile(w.t0);
+  if (warp == 10 && lane == 0) {
+    load_q<D, NR>(p, &tm_q, smem + C::kQ, q_full, tile, w.b, w.g);
+    load_tile(w.t0);
+  }
+  // Rows of Q's buffer that no load fills.
+  const int tile_fill = p.parts == 1 ? p.tile_t * p.G : NR;
+  for (int i = threadIdx.x; i < (NR - tile_fill) * (D / 8); i += C::kThreads)
+    *reinterpret_cast<uint4*>(smem + C::kQ + (i % (D / 8) >> 3) * (NR * 128) + (tile_fill + i / (D / 8)) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   if (warp == 8) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
@@ -834,6 +839,19 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
           volatile int no_abort = 0;
           for (int j = loads_k > RING ? loads_k - RING : 0; j < loads_k; ++j) mbar_wait(&k_full[j % RING], (j / RING) & 1, &no_abort);
           for (int j = tiles > RING ? tiles - RING : 0; j < tiles; ++j) mbar_wait(&v_full[j % RING], (j / RING) & 1, &no_abort);
+        }
+      }
+    } else if (warp == 11) {
+      // =================== TMA of the next pairs' Q ===================
+      if (lane == 0) {
+        int seg = 0;  // of the last load
+        while (w.next(ln) && mbar_wait(q_empty, seg & 1, s_abort)) {
+          load_q<D, NR>(p, &tm_q, smem + C::kQ, q_full, tile, w.b, w.g);
+          ++seg;
+        }
+        if (*s_abort) {
+          volatile int no_abort = 0;
+          mbar_wait(q_full, seg & 1, &no_abort);
         }
       }
     } else if (warp == 8) {
@@ -892,6 +910,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
             if (lane == 0) mbar_arrive(&pv_done[n & 1]);  // (orders sBad before the epilogue)
           }
         }
+        umma_commit(q_empty);  // (after the pair's last S)
         ++seg;
       } while (ok && w.next(ln));
       umma_commit(drain);
@@ -903,21 +922,10 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
     // =================== softmax and epilogue: a thread per row ===================
     // (A failed wait raises *s_abort and the thread runs on, as in mfa_tree_kernel.)
     const int grp = warp >> 2, quad = warp & 3;
-    const int r = quad * 32 + lane, row = rt * NR + r;  // the thread's row of the tile, of the pair
-    const bool real = row < p.R;
+    const int r = quad * 32 + lane, row = tile.row0 + r;  // the thread's row of the tile, of the pair
+    const bool real = r < tile.rows;
     const int node = real ? p.by_g(row) : 0, head = row - node * p.G;
     const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    auto store_q = [&]() {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int x = qr + k * kStep;
-        if (rt * NR + x >= p.R) qy[k] = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(smem + C::kQ + (qu >> 3) * kChunk + x * 128 + (((qu & 7) ^ (x & 7)) << 4)) = qy[k];
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(q_full);
-    };
-    store_q();
     int n = 0;  // tiles of the CTA before the pair's first
     uint32_t lasts = 0;  // of the group's last P.V of a pair
     do {
@@ -1018,14 +1026,9 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[grp]);
       }
-      // Q of the next pair once every S of this one is done: this group's last, and by the
-      // barrier below the other's.
       Walk nx = w;
       const bool more = nx.next(ln);
-      if (more) {
-        fetch_parent(nx.b);
-        fetch_q(nx.b, nx.g);
-      }
+      if (more) fetch_parent(nx.b);
 
       // ---- epilogue of the pair: merge the groups ----
       const int end = n + count;
@@ -1038,7 +1041,6 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
       sL[grp * 128 + r] = l;
       named_barrier(1, 256);
       tc_fence_after();
-      if (more) store_q();
       {
         const float m0 = sM[r], m1 = sM[128 + r], l0 = sL[r], l1 = sL[128 + r];
         const float M = fmaxf(m0, m1);  // (-inf: no key seen, or only NaN scores)
@@ -1126,10 +1128,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
   const int r = SPLIT ? blockIdx.y / p.rtiles : blockIdx.y / p.rtiles * kMergeWarps + warp;  // row of the row tile
   const int b = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (r >= min(NR, p.R - rt * NR)) return;  // (SPLIT: the whole block)
+  const RowTile tile(p, rt, NR);
+  if (r >= tile.rows) return;  // (SPLIT: the whole block)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // The CTAs that met the pair.
-  const Line ln{p.lens, p.B, p.Hkv, p.N, last_node<NR>(p, rt), EXTRA};
+  const Line ln{p.lens, p.B, p.Hkv, p.N, tile.last_node(p), EXTRA};
   int before = 0, total = 0;
   for (int x = lane; x < p.B; x += 32) {
     const int n = ln.tiles(ln.len(x)) + ln.extra;
@@ -1193,7 +1196,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
 #pragma unroll
       for (int x = 1; x < kMergeWarps; ++x) o[e] += so[x][lane * E + e];
   }
-  const int row = rt * NR + r, t = p.by_g(row), h = g * p.G + row - t * p.G;
+  const int row = tile.row0 + r, t = p.by_g(row), h = g * p.G + row - t * p.G;
   const bool has = l != 0.f;
   const float inv = has ? 1.f / l : 0.f;
   uint32_t* to = reinterpret_cast<uint32_t*>(p.out + b * p.os[0] + h * p.os[1] + t * p.os[2] + lane * E);
@@ -1210,19 +1213,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
 // ---- host ----
 
 struct TreePlan {
-  int nr, rtiles, groups;
+  int nr, rtiles, groups, tile_t, parts;
 };
 
-// Rows per tile: the smallest of 16, 32, 64, 128 (D = 256: 64) that holds the R rows, or the
-// largest and several tiles. CTAs: one per SM, the row tiles side by side on the same keys; with
-// more than 8 row tiles about two per SM instead, so that an uneven number of
-// tiles costs less than the half-empty last wave.
-TreePlan plan_tree(int64_t R, int64_t D) {
+// Rows per tile: the smallest of 16, 32, 64, 128 (D = 256: 64) that holds the
+// T nodes' rows, or the largest and several tiles of whole nodes (of parts of one node's
+// heads where G exceeds a tile). CTAs: one per SM, the row tiles side by side
+// on the same keys; with more than 8 row tiles about two per SM instead, so
+// that an uneven number of tiles costs less than the half-empty last wave.
+TreePlan plan_tree(int64_t T, int64_t G, int64_t D) {
   const int n_sm = device_sm_count();
-  const int64_t sms = n_sm > 0 ? n_sm : 148;
+  const int64_t sms = n_sm > 0 ? n_sm : 148, R = T * G;
   TreePlan pl;
   pl.nr = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 || D == 256 ? 64 : kMaxRows;
-  pl.rtiles = static_cast<int>(cdiv64(R, pl.nr));
+  pl.parts = static_cast<int>(cdiv64(G, pl.nr));
+  pl.tile_t = pl.parts > 1 ? 1 : static_cast<int>(T < pl.nr / G ? T : pl.nr / G);
+  pl.rtiles = static_cast<int>(pl.parts > 1 ? T * pl.parts : cdiv64(T, pl.tile_t));
   pl.groups = static_cast<int>(pl.rtiles <= 8 ? sms / pl.rtiles : cdiv64(2 * sms, pl.rtiles));
   if (pl.groups < 1) pl.groups = 1;
   return pl;
@@ -1235,14 +1241,28 @@ size_t part_bytes(const TreePlan& pl, int64_t D, size_t* o_bytes) {
   return *o_bytes + align256(rows * 2 * 4) + 256;
 }
 
+// The tensor map of q: boxes of 64 columns x the heads of a group x the nodes of a row tile.
+bool map_queries(CUtensorMap* map, const mfa_tensor* q, const TreePlan& pl, int64_t G) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(q->D), static_cast<cuuint64_t>(q->H), static_cast<cuuint64_t>(q->N),
+                        static_cast<cuuint64_t>(q->B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(q->stride[1]) * 2, static_cast<cuuint64_t>(q->stride[2]) * 2,
+                           static_cast<cuuint64_t>(q->stride[0]) * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(pl.parts > 1 ? pl.nr : G), static_cast<cuuint32_t>(pl.tile_t), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, q->data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int NR, int EXTRA, typename K>
-mfa_status launch_tree(K kernel, int threads, int bytes, std::atomic<uint64_t>& attr_devs, const CUtensorMap& mk, const CUtensorMap& mv,
-                       const TreeParams& p, cudaStream_t s) {
+mfa_status launch_tree(K kernel, int threads, int bytes, std::atomic<uint64_t>& attr_devs, const CUtensorMap& mq, const CUtensorMap& mk,
+                       const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), bytes, attr_devs)) return MFA_ERR_CUDA;
-  if (!launch_after(kernel, dim3(static_cast<unsigned>(p.rtiles) * p.groups), threads, bytes, s, mk, mv, p)) return MFA_ERR_CUDA;
+  if (!launch_after(kernel, dim3(static_cast<unsigned>(p.rtiles) * p.groups), threads, bytes, s, mq, mk, mv, p)) return MFA_ERR_CUDA;
   if (p.groups > 1) {
     const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
-    const int rows = p.R < NR ? p.R : NR;
+    const int rows = p.parts > 1 ? NR : p.tile_t * p.G;  // of a tile
     const bool split = pairs * p.R <= 1024;
     const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>((split ? rows : cdiv64(rows, kMergeWarps)) * p.rtiles));
     if (!launch_after(split ? mfa_tree_merge<D, NR, EXTRA, true> : mfa_tree_merge<D, NR, EXTRA, false>, grid, kMergeWarps * 32, 0, s, p))
@@ -1252,28 +1272,28 @@ mfa_status launch_tree(K kernel, int threads, int bytes, std::atomic<uint64_t>& 
 }
 
 template <int D, int NR>
-mfa_status launch_keys(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
+mfa_status launch_keys(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
   using C = Cfg<D, NR>;
   static std::atomic<uint64_t> attr_devs{0};
-  return launch_tree<D, NR, C::kExtra>(mfa_tree_kernel<D, NR>, C::kThreads, C::kBytes, attr_devs, mk, mv, p, s);
+  return launch_tree<D, NR, C::kExtra>(mfa_tree_kernel<D, NR>, C::kThreads, C::kBytes, attr_devs, mq, mk, mv, p, s);
 }
 
 template <int D>
-mfa_status launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
+mfa_status launch_rows(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
   using C = RowCfg<D>;
   static std::atomic<uint64_t> attr_devs{0};
-  return launch_tree<D, 128, C::kExtra>(mfa_tree_rows_kernel<D>, C::kThreads, C::kBytes, attr_devs, mk, mv, p, s);
+  return launch_tree<D, 128, C::kExtra>(mfa_tree_rows_kernel<D>, C::kThreads, C::kBytes, attr_devs, mq, mk, mv, p, s);
 }
 
 template <int D>
-mfa_status launch_tree_rows(int nr, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
+mfa_status launch_tree_rows(int nr, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
   switch (nr) {
-    case 16: return launch_keys<D, 16>(mk, mv, p, s);
-    case 32: return launch_keys<D, 32>(mk, mv, p, s);
-    case 64: return launch_keys<D, 64>(mk, mv, p, s);
+    case 16: return launch_keys<D, 16>(mq, mk, mv, p, s);
+    case 32: return launch_keys<D, 32>(mq, mk, mv, p, s);
+    case 64: return launch_keys<D, 64>(mq, mk, mv, p, s);
     default:
       if constexpr (D == 256) return MFA_ERR_UNSUPPORTED;  // plan_tree gives no such tile
-      else return launch_rows<D>(mk, mv, p, s);
+      else return launch_rows<D>(mq, mk, mv, p, s);
   }
 }
 
@@ -1285,7 +1305,7 @@ extern "C" size_t mfa_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t
   if (B < 0 || Hq <= 0 || Hkv <= 0 || T < 0 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
   if (B == 0 || T == 0) return 256;
   size_t o_bytes;
-  return part_bytes(plan_tree(static_cast<int64_t>(T) * (Hq / Hkv), D), D, &o_bytes);
+  return part_bytes(plan_tree(T, Hq / Hkv, D), D, &o_bytes);
 }
 
 extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, const mfa_tensor* v,
@@ -1302,30 +1322,27 @@ extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, 
   if (out->B != q->B || out->H != q->H || out->N != q->N || out->D != q->D) return MFA_ERR_SHAPE_MISMATCH;
   if (empty) return MFA_OK;
   const int64_t R = q->N * (q->H / k->H);
-  const TreePlan pl = plan_tree(R, q->D);
+  const TreePlan pl = plan_tree(q->N, q->H / k->H, q->D);
   size_t o_bytes;
   const size_t need = part_bytes(pl, q->D, &o_bytes);
   if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
     return MFA_ERR_INVALID_ARG;
-  CUtensorMap mk, mv;
-  if (!map_keys(&mk, k) || !map_keys(&mv, v)) return MFA_ERR_CUDA;
+  CUtensorMap mq, mk, mv;
+  if (!map_queries(&mq, q, pl, q->H / k->H) || !map_keys(&mk, k) || !map_keys(&mv, v)) return MFA_ERR_CUDA;
   TreeParams p;
   p.B = static_cast<int32_t>(q->B); p.Hq = static_cast<int32_t>(q->H); p.Hkv = static_cast<int32_t>(k->H);
   p.G = static_cast<int32_t>(q->H / k->H); p.T = static_cast<int32_t>(q->N); p.N = static_cast<int32_t>(k->N);
   p.R = static_cast<int32_t>(R);
   p.by_g.set(static_cast<uint32_t>(p.G));
-  p.rtiles = pl.rtiles; p.groups = pl.groups;
+  p.rtiles = pl.rtiles; p.groups = pl.groups; p.tile_t = pl.tile_t; p.parts = pl.parts;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(q->D)));
-  p.q = static_cast<const __nv_bfloat16*>(q->data);
-  for (int a = 0; a < 3; ++a) {
-    p.qs[a] = q->stride[a]; p.os[a] = out->stride[a];
-  }
+  for (int a = 0; a < 3; ++a) p.os[a] = out->stride[a];
   p.lens = lens; p.parents = parents;
   p.out = static_cast<__nv_bfloat16*>(out->data); p.lse = lse; p.err = dev_err;
   p.o_part = static_cast<float*>(workspace);
   p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + o_bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (q->D == 64) return launch_tree_rows<64>(pl.nr, mk, mv, p, s);
-  if (q->D == 128) return launch_tree_rows<128>(pl.nr, mk, mv, p, s);
-  return launch_tree_rows<256>(pl.nr, mk, mv, p, s);
+  if (q->D == 64) return launch_tree_rows<64>(pl.nr, mq, mk, mv, p, s);
+  if (q->D == 128) return launch_tree_rows<128>(pl.nr, mq, mk, mv, p, s);
+  return launch_tree_rows<256>(pl.nr, mq, mk, mv, p, s);
 }

@@ -47,6 +47,10 @@ CASES = [
     (128, 16, 1, 2, 260, [258] + [7 * i for i in range(30)], "random", True),
     (128, 1, 16, 1, 4000, [3999], None, False),             # one sequence over every SM
     (64, 1, 32, 1, 9000, [8999], None, True),
+    (64, 1, 150, 3, 700, [697, 200], "random", True),       # a group larger than a row tile
+    (256, 2, 70, 2, 300, [290, 0], None, False),
+    (128, 1, 7, 20, 900, [850, 3], "random", True),         # 140 rows, 126 in the first tile
+    (128, 2, 5, 3, 400, [390], "random", False),            # 15 rows of 16
 ]
 
 
