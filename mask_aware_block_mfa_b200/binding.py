@@ -516,21 +516,25 @@ class _CacheOp:
         """Memory allocated for a call belongs to the call's stream."""
         return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
-    def _call(self, name: str, fn, *args, stream=None):
-        """Call an entry point on `stream` with the object's device current."""
-        index = self.device.index
+    def _stream(self, stream) -> int:
+        """The handle of `stream` (None: the device's current one); the object's tensors are in use there."""
         if stream is None:
-            ptr = torch._C._cuda_getCurrentRawStream(index)
+            ptr = torch._C._cuda_getCurrentRawStream(self.device.index)
         else:
             ptr = _stream_ptr(stream, self.device)
         for t, home in self._kept:
             if ptr != home:
                 t.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+        return ptr
+
+    def _call(self, name: str, fn, *args):
+        """Call an entry point with the object's device current."""
+        index = self.device.index
         if torch._C._cuda_getDevice() == index:
-            code = fn(*args, ptr)
+            code = fn(*args)
         else:
             with torch.cuda.device(index):
-                code = fn(*args, ptr)
+                code = fn(*args)
         if code != MFA_OK:
             _check(name, code)
 
@@ -581,7 +585,7 @@ class TreeDecode(_CacheOp):
         od = _cache_desc("out", out, dev, q.shape)
         lse_p = _array_ptr("lse", lse, dev, torch.float32, (B_, Hq, T))
         self._call("mfa_tree_decode", _cache_fns().mfa_tree_decode, qd, kd, vd, lens_p, par_p, od, lse_p, self._ws,
-                   self._ws_bytes, self._err, stream=stream)
+                   self._ws_bytes, self._err, self._stream(stream))
         return out, lse
 
 
@@ -608,7 +612,7 @@ class KeyWeights(_CacheOp):
                 weights_out = torch.zeros(shape, dtype=torch.float32, device=dev)
         out_p = _array_ptr("weights_out", weights_out, dev, torch.float32, shape)
         self._call("mfa_key_weights", _cache_fns().mfa_key_weights, qd, kd, lse_p, lens_p, par_p, row_p, in_p, float(decay),
-                   out_p, self._err, stream=stream)
+                   out_p, self._err, self._stream(stream))
         return weights_out
 
 
@@ -621,30 +625,40 @@ class CacheCompact(_CacheOp):
         place, or in k_out, v_out (and weights_out). idx int32 [B, Hkv or 1, n]; count, start and
         zero_end int32 [B]. With start = lens and the accepted nodes, ascending, a branch of a
         tree is committed; the caller then adds count to lens."""
+        kd, vd, w_p, zero_p, kod, vod, wo_p, B_, H, _ = self._tensors(k, v, weights, zero_end, k_out, v_out, weights_out)
+        dev = self.device
+        if not isinstance(idx, torch.Tensor) or idx.dim() != 3 or idx.shape[1] not in (1, H):
+            raise ValueError("idx must be an int32 [B, Hkv or 1, n] tensor")
+        idx_p = _array_ptr("idx", idx, dev, torch.int32, (B_, idx.shape[1], idx.shape[2]))
+        count_p = _array_ptr("count", count, dev, torch.int32, (B_,))
+        start_p = None if start is None else _array_ptr("start", start, dev, torch.int32, (B_,))
+        self._call("mfa_cache_compact", _cache_fns().mfa_cache_compact, kd, vd, w_p, start_p, idx_p, idx.shape[1],
+                   idx.shape[2], count_p, zero_p, kod, vod, wo_p, self._err, self._stream(stream))
+
+    def _tensors(self, k, v, weights, zero_end, k_out, v_out, weights_out):
+        """Descriptors and addresses of what is moved, checked, and k's sizes B, H, N."""
         dev = self.device
         if (k_out is None) != (v_out is None):
             raise ValueError("k_out and v_out are given together")
         if k_out is not None and (weights is None) != (weights_out is None):
             raise ValueError("weights and weights_out are given together")
-        kd, vd = _cache_desc("k", k, dev), _cache_desc("v", v, dev, k.shape)
+        kd = _cache_desc("k", k, dev)
+        vd = _cache_desc("v", v, dev, k.shape)
         B_, H, N, _ = k.shape
         if k_out is None:
             if weights_out is not None:
                 raise ValueError("weights_out without k_out and v_out")
             kod, vod, weights_out, N_out = kd, vd, weights, N
         else:
-            kod, vod = _cache_desc("k_out", k_out, dev), _cache_desc("v_out", v_out, dev, k_out.shape)
+            kod = _cache_desc("k_out", k_out, dev)
+            vod = _cache_desc("v_out", v_out, dev, k_out.shape)
             N_out = k_out.shape[2]
-        if idx.dim() != 3 or idx.shape[1] not in (1, H):
-            raise ValueError("idx must be an int32 [B, Hkv or 1, n] tensor")
-        idx_p = _array_ptr("idx", idx, dev, torch.int32, (B_, idx.shape[1], idx.shape[2]))
-        count_p = _array_ptr("count", count, dev, torch.int32, (B_,))
-        start_p = None if start is None else _array_ptr("start", start, dev, torch.int32, (B_,))
+        w_p = wo_p = None
+        if weights is not None:
+            w_p = _array_ptr("weights", weights, dev, torch.float32, (B_, H, N))
+            wo_p = w_p if weights_out is weights else _array_ptr("weights_out", weights_out, dev, torch.float32, (B_, H, N_out))
         zero_p = None if zero_end is None else _array_ptr("zero_end", zero_end, dev, torch.int32, (B_,))
-        w_p = None if weights is None else _array_ptr("weights", weights, dev, torch.float32, (B_, H, N))
-        wo_p = None if weights is None else _array_ptr("weights_out", weights_out, dev, torch.float32, (B_, H, N_out))
-        self._call("mfa_cache_compact", _cache_fns().mfa_cache_compact, kd, vd, w_p, start_p, idx_p, idx.shape[1],
-                   idx.shape[2], count_p, zero_p, kod, vod, wo_p, self._err, stream=stream)
+        return kd, vd, w_p, zero_p, kod, vod, wo_p, B_, H, N
 
 
 class Evictor(_CacheOp):
@@ -653,43 +667,52 @@ class Evictor(_CacheOp):
     of the largest weight (mfa_evict_select, then mfa_cache_compact)."""
 
     def __init__(self, budget: int, recent: int, device="cuda"):
+        if budget < 1 or not 0 <= recent <= budget:
+            raise ValueError(f"budget must be at least 1 and recent in [0, budget], got {budget} and {recent}")
         super().__init__(device)
         self.budget, self.recent = int(budget), int(recent)
         self.compact = CacheCompact(device)
         self.compact.err, self.compact._err, self.compact._kept = self.err, self._err, self._kept
 
-    def _lists(self, B_, H, keep, new_lens):
+    def _lists(self, lens, H, stream, keep=None, new_lens=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._lists(lens, H, None, keep, new_lens)
         if keep is None:
-            keep = torch.empty(B_, H, self.budget, dtype=torch.int32, device=self.device)
+            keep = lens.new_empty((lens.shape[0], H, self.budget))
         if new_lens is None:
-            new_lens = torch.empty(B_, dtype=torch.int32, device=self.device)
+            new_lens = torch.empty_like(lens)
         return keep, new_lens
 
     def select(self, weights, lens, keep=None, new_lens=None, stream=None):
         """keep int32 [B, Hkv, budget] (ascending rows, then -1) and new_lens int32 [B]."""
         dev = self.device
-        if weights.dim() != 3:
+        if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
             raise ValueError("weights must be a float32 [B, Hkv, N] tensor")
         B_, H, N = weights.shape
         w_p = _array_ptr("weights", weights, dev, torch.float32, (B_, H, N))
         lens_p = _array_ptr("lens", lens, dev, torch.int32, (B_,))
         if keep is None or new_lens is None:
-            if stream is None:
-                keep, new_lens = self._lists(B_, H, keep, new_lens)
-            else:
-                with torch.cuda.stream(stream):
-                    keep, new_lens = self._lists(B_, H, keep, new_lens)
+            keep, new_lens = self._lists(lens, H, stream, keep, new_lens)
         keep_p = _array_ptr("keep", keep, dev, torch.int32, (B_, H, self.budget))
         new_p = _array_ptr("new_lens", new_lens, dev, torch.int32, (B_,))
         self._call("mfa_evict_select", _cache_fns().mfa_evict_select, w_p, lens_p, B_, H, N, self.budget, self.recent,
-                   keep_p, new_p, self._err, stream=stream)
+                   keep_p, new_p, self._err, self._stream(stream))
         return keep, new_lens
 
     def __call__(self, k, v, weights, lens, k_out=None, v_out=None, weights_out=None, zero_end=None, stream=None):
         """Select, then move the kept rows of k, v and weights together, in place or into
         k_out, v_out and weights_out. Returns keep and new_lens; lens is left to the caller."""
-        keep, new_lens = self.select(weights, lens, stream=stream)
-        self.compact(k, v, keep, new_lens, weights, None, zero_end, k_out, v_out, weights_out, stream=stream)
+        if weights is None:
+            raise ValueError("weights must be a float32 [B, Hkv, N] tensor")
+        kd, vd, w_p, zero_p, kod, vod, wo_p, B_, H, N = self.compact._tensors(k, v, weights, zero_end, k_out, v_out, weights_out)
+        lens_p = _array_ptr("lens", lens, self.device, torch.int32, (B_,))
+        keep, new_lens = self._lists(lens, H, stream)
+        keep_p, new_p, s, fns = keep.data_ptr(), new_lens.data_ptr(), self._stream(stream), _cache_fns()
+        self._call("mfa_evict_select", fns.mfa_evict_select, w_p, lens_p, B_, H, N, self.budget, self.recent, keep_p,
+                   new_p, self._err, s)
+        self._call("mfa_cache_compact", fns.mfa_cache_compact, kd, vd, w_p, None, keep_p, H, self.budget, new_p, zero_p,
+                   kod, vod, wo_p, self._err, s)
         return keep, new_lens
 
 
