@@ -48,12 +48,14 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 constexpr uint32_t kZeroKey = 0x80000000u;
 
 // SHARED: the keys in shared memory; otherwise read again for each pass.
-template <bool SHARED>
+// LIST: the kept keys' rows are put in order in shared memory too, and written from
+// there side by side (64 lists of 8192 of 32768: 3 us less than scattered writes).
+template <bool SHARED, bool LIST>
 __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ int hist[3][kBins];
   __shared__ int s_sum[kSelWarps], s_gt[kSelWarps], s_eq[kSelWarps];
   __shared__ int s_bin, s_left;
-  extern __shared__ __align__(16) uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];  // the keys; with LIST the kept ones' rows behind them
   for (int i = threadIdx.x; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
   const int seg = (m + kSelWarps * kRun - 1) / (kSelWarps * kRun) * kRun, j0 = warp * seg;
   uint32_t* own = s_keys + j0;
   if constexpr (SHARED) {
-#pragma unroll 16
+#pragma unroll 8
     for (int i = lane; i < seg; i += 32) own[i] = j0 + i < m ? order_key(__ldg(w + j0 + i)) : 0u;
   }
   __syncthreads();
@@ -104,6 +106,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 31 : pass == 1 ? 21 : 10;
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    const bool has_zero = pass == 0 || (kZeroKey >> above) == prefix;  // zero may be among the keys counted
     int zeros = 0;
 #pragma unroll 2
     for (int i = 0; i < seg; i += kRun) {
@@ -118,17 +121,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
         any |= in[y];
       }
       if (pass > 0 && !__any_sync(0xffffffffu, any)) continue;  // few keys get past the first digit
-      const int first = __shfl_sync(0xffffffffu, bin[0], 0);
-      const bool same = in[0] && in[1] && in[2] && in[3] && bin[0] == first && bin[1] == first && bin[2] == first && bin[3] == first;
-      if (__all_sync(0xffffffffu, same)) {
-        if (lane == 0) atomicAdd(&hist[pass][first], kRun);
-        continue;
+      if (__all_sync(0xffffffffu, in[0] && in[1] && in[2] && in[3])) {
+        const int first = __shfl_sync(0xffffffffu, bin[0], 0);
+        if (__all_sync(0xffffffffu, bin[0] == first && bin[1] == first && bin[2] == first && bin[3] == first)) {
+          if (lane == 0) atomicAdd(&hist[pass][first], kRun);
+          continue;
+        }
       }
+      if (has_zero) {
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        if (!in[y]) continue;
-        if (key[y] == kZeroKey) ++zeros;
-        else atomicAdd(&hist[pass][bin[y]], 1);
+        for (int y = 0; y < 4; ++y) {
+          zeros += in[y] && key[y] == kZeroKey;
+          if (in[y] && key[y] != kZeroKey) atomicAdd(&hist[pass][bin[y]], 1);
+        }
+      } else {
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (in[y]) atomicAdd(&hist[pass][bin[y]], 1);
       }
     }
     zeros = __reduce_add_sync(0xffffffffu, zeros);
@@ -178,7 +187,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
     s_eq[warp] = eq;
   }
   __syncthreads();
-  if (gt + eq == 0) return;  // (of this warp)
+  int32_t* list = LIST ? reinterpret_cast<int32_t*>(s_keys + seg * kSelWarps) : keep;
   gt = __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
   eq = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
   // A kept key's place: the keys above the k-th before it, and the equal ones that are kept.
@@ -208,10 +217,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
       const bool is_gt = key[y] > prefix, is_eq = key[y] == prefix;
-      if (is_gt || (is_eq && ties < left)) keep[at + min(ties, left)] = j + y;
+      if (is_gt || (is_eq && ties < left)) list[at + min(ties, left)] = j + y;
       at += is_gt;
       ties += is_eq;
     }
+  }
+  if constexpr (LIST) {
+    __syncthreads();
+    for (int t = threadIdx.x; t < k; t += kSelThreads) keep[t] = list[t];
   }
 }
 
@@ -414,12 +427,16 @@ extern "C" mfa_status mfa_evict_select(const float* weights, const int32_t* lens
   const int64_t keys = cdiv64(N, kSelWarps * kRun) * kSelWarps * kRun;  // with every warp's run full
   const dim3 grid(Hkv, B);
   bool ok;
-  if (keys <= kSelShared) {
+  if (keys + budget <= kSelShared) {
     static std::atomic<uint64_t> attr_devs{0};
-    if (!ensure_smem_attr(reinterpret_cast<const void*>(mfa_select_kernel<true>), kSelShared * 4, attr_devs)) return MFA_ERR_CUDA;
-    ok = launch_after(mfa_select_kernel<true>, grid, kSelThreads, static_cast<size_t>(keys) * 4, cs, p);
+    if (!ensure_smem_attr(reinterpret_cast<const void*>(mfa_select_kernel<true, true>), kSelShared * 4, attr_devs)) return MFA_ERR_CUDA;
+    ok = launch_after(mfa_select_kernel<true, true>, grid, kSelThreads, static_cast<size_t>(keys + budget) * 4, cs, p);
+  } else if (keys <= kSelShared) {
+    static std::atomic<uint64_t> attr_devs{0};
+    if (!ensure_smem_attr(reinterpret_cast<const void*>(mfa_select_kernel<true, false>), kSelShared * 4, attr_devs)) return MFA_ERR_CUDA;
+    ok = launch_after(mfa_select_kernel<true, false>, grid, kSelThreads, static_cast<size_t>(keys) * 4, cs, p);
   } else {
-    ok = launch_after(mfa_select_kernel<false>, grid, kSelThreads, 0, cs, p);
+    ok = launch_after(mfa_select_kernel<false, false>, grid, kSelThreads, 0, cs, p);
   }
   return ok ? MFA_OK : MFA_ERR_CUDA;
 }
