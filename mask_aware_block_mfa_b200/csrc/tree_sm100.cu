@@ -717,7 +717,7 @@ template <int D>
 struct RowCfg {
   static constexpr int kExtra = 10;  // (2 to 14 measured over 12 cases of 96 to 496 rows: within 3% from 7 on)
   static constexpr int kThreads = 384;                  // two softmax groups; MMA, TMA of K and V, TMA of Q, an idle one
-  static constexpr int kRegsLow = 96, kRegsHigh = 200;  // 384 x 168 >= 128 x 96 + 256 x 200
+  static constexpr int kRegsLow = 104, kRegsHigh = 200;  // 384 x 168 = 128 x 104 + 256 x 200
   static constexpr int kTile = D / 64 * kChunk;         // K or V of a tile
   static constexpr int kRing = D == 64 ? 5 : 3;         // tiles of each
   static constexpr int kQ = 0;                          // 128 rows x 128 B per 64 columns
@@ -1005,18 +1005,18 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(-m_use, -m_use);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
+          for (int c = 0; c < 16; ++c) {
             float a, b;
-            f2_unpack(f2_fma(f2_pack(x[h * 64 + 2 * c], x[h * 64 + 2 * c + 1]), sc2, nm2), a, b);
+            f2_unpack(f2_fma(f2_pack(x[h * 32 + 2 * c], x[h * 32 + 2 * c + 1]), sc2, nm2), a, b);
             a = ex2_approx(a);
             b = ex2_approx(b);
             sum[c & 1] = f2_add(sum[c & 1], f2_pack(a, b));
             pk[c] = pack_bf16x2(a, b);
           }
-          tmem_st_32x32b_x32(tm + grp * 128 + h * 32, pk);
+          tmem_st_32x32b_x16(tm + grp * 128 + h * 16, pk);
         }
         float a, b;
         f2_unpack(f2_add(sum[0], sum[1]), a, b);
