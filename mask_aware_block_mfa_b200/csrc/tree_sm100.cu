@@ -977,46 +977,62 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
           for (int c = 0; c < kKeys; ++c)
             if (!(see[c >> 5] >> (c & 31) & 1)) x[c] = -INFINITY;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 8) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) mx[y] = fmax3(mx[y], x[c + 2 * y], x[c + 2 * y + 1]);
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        const bool need = top > m + kLazy;
-        const float m_new = need ? top : m, m_use = m_new == -INFINITY ? 0.f : m_new;
-        if (i >= 2 && __any_sync(0xffffffffu, need)) {
-          // Rare: the row's sums so far shrink. O holds every P.V of the group before
-          // this tile's: S(k) went out after P.V(k - 2).
-          const float alpha = need ? ex2_approx(m - m_use) : 1.f;  // (m = -inf: 0, and the sums are 0)
-          l *= alpha;
+        // The weights are computed relative to the maximum so far while the tile's own is found:
+        // it seldom moves (a group's first tile finds it first). Where one does, the
+        // row's sums shrink and the warp computes the tile's weights again.
+        uint64_t sum[2];
+        bool again = i < 2;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(tm + C::kO + grp * D + c, o);
-            tmem_ld_wait();
+        while (true) {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (again) {
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
-            tmem_st_32x32b_x32(tm + C::kO + grp * D + c, o);
+            for (int c = 0; c < kKeys; c += 8) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) mx[y] = fmax3(mx[y], x[c + 2 * y], x[c + 2 * y + 1]);
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+            const bool need = top > m + kLazy;
+            const float m_new = need ? top : m;
+            if (i >= 2) {
+              // O holds every P.V of the group before this tile's: S(k) went out after P.V(k - 2).
+              const float alpha = need ? ex2_approx(m - m_new) : 1.f;  // (m = -inf: 0, and the sums are 0)
+              l *= alpha;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(tm + C::kO + grp * D + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+                tmem_st_32x32b_x32(tm + C::kO + grp * D + c, o);
+              }
+            }
+            m = m_new;
           }
-        }
-        m = m_new;
-        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(-m_use, -m_use);
-        uint64_t sum[2] = {0ull, 0ull};
+          const float m_use = m == -INFINITY ? 0.f : m;
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(-m_use, -m_use);
+          sum[0] = sum[1] = 0ull;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t pk[16];
+          for (int h = 0; h < 4; ++h) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            float a, b;
-            f2_unpack(f2_fma(f2_pack(x[h * 32 + 2 * c], x[h * 32 + 2 * c + 1]), sc2, nm2), a, b);
-            a = ex2_approx(a);
-            b = ex2_approx(b);
-            sum[c & 1] = f2_add(sum[c & 1], f2_pack(a, b));
-            pk[c] = pack_bf16x2(a, b);
+            for (int c = 0; c < 16; ++c) {
+              const int y = h * 32 + 2 * c;
+              float a, b;
+              f2_unpack(f2_fma(f2_pack(x[y], x[y + 1]), sc2, nm2), a, b);
+              a = ex2_approx(a);
+              b = ex2_approx(b);
+              mx[c & 3] = fmax3(mx[c & 3], x[y], x[y + 1]);
+              sum[c & 1] = f2_add(sum[c & 1], f2_pack(a, b));
+              pk[c] = pack_bf16x2(a, b);
+            }
+            tmem_st_32x32b_x16(tm + grp * 128 + h * 16, pk);
           }
-          tmem_st_32x32b_x16(tm + grp * 128 + h * 16, pk);
+          if (again) break;
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          if (!__any_sync(0xffffffffu, top > m + kLazy)) break;
+          again = true;
         }
         float a, b;
         f2_unpack(f2_add(sum[0], sum[1]), a, b);
