@@ -417,7 +417,12 @@ mfa_status mfa_decode(const mfa_tensor* q, const mfa_tensor* k, const mfa_tensor
  * ends there).
  * Cache rows at or past lens[b] + T, padding nodes' rows and masked nodes' keys
  * may hold anything, infinities and NaN included. A row that sees a DRAFTED
- * key whose value row holds an infinity or a NaN gets NaN in all D columns. */
+ * key whose value row holds an infinity or a NaN gets NaN in all D columns.
+ * Outputs share no memory with a call's inputs, or with one another, unless
+ * that is said. The kernels' waits are bounded (2 s): one that runs out sets
+ * MFA_DEVERR_TIMEOUT, and the call's outputs are then undefined.
+ * Sizes beyond B * Hq * T < 2^30, B * Hkv * (ceil(N / 128) + 16) < 2^30, T < 2^24 or
+ * B, Hq <= 65535 are MFA_ERR_UNSUPPORTED. */
 
 /* Largest T with a tree (parents != NULL). */
 #define MFA_TREE_MAX_NODES 256

@@ -527,6 +527,14 @@ class _CacheOp:
                 t.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
         return ptr
 
+    @staticmethod
+    def _lend(stream, *tensors):
+        """The caller's tensors are in use on a stream given by name: their memory is not
+        handed out again before that work is done."""
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
     def _call(self, name: str, fn, *args):
         """Call an entry point with the object's device current."""
         index = self.device.index
@@ -584,6 +592,8 @@ class TreeDecode(_CacheOp):
                     lse = torch.empty(B_, Hq, T, dtype=torch.float32, device=dev)
         od = _cache_desc("out", out, dev, q.shape)
         lse_p = _array_ptr("lse", lse, dev, torch.float32, (B_, Hq, T))
+        if stream is not None:
+            self._lend(stream, q, k, v, lens, parents, out, lse)
         self._call("mfa_tree_decode", _cache_fns().mfa_tree_decode, qd, kd, vd, lens_p, par_p, od, lse_p, self._ws,
                    self._ws_bytes, self._err, self._stream(stream))
         return out, lse
@@ -611,6 +621,8 @@ class KeyWeights(_CacheOp):
             with self._on_stream(stream):
                 weights_out = torch.zeros(shape, dtype=torch.float32, device=dev)
         out_p = _array_ptr("weights_out", weights_out, dev, torch.float32, shape)
+        if stream is not None:
+            self._lend(stream, q, k, lse, lens, parents, row_scale, weights_in, weights_out)
         self._call("mfa_key_weights", _cache_fns().mfa_key_weights, qd, kd, lse_p, lens_p, par_p, row_p, in_p, float(decay),
                    out_p, self._err, self._stream(stream))
         return weights_out
@@ -632,6 +644,8 @@ class CacheCompact(_CacheOp):
         idx_p = _array_ptr("idx", idx, dev, torch.int32, (B_, idx.shape[1], idx.shape[2]))
         count_p = _array_ptr("count", count, dev, torch.int32, (B_,))
         start_p = None if start is None else _array_ptr("start", start, dev, torch.int32, (B_,))
+        if stream is not None:
+            self._lend(stream, k, v, weights, zero_end, k_out, v_out, weights_out, idx, count, start)
         self._call("mfa_cache_compact", _cache_fns().mfa_cache_compact, kd, vd, w_p, start_p, idx_p, idx.shape[1],
                    idx.shape[2], count_p, zero_p, kod, vod, wo_p, self._err, self._stream(stream))
 
@@ -696,6 +710,8 @@ class Evictor(_CacheOp):
             keep, new_lens = self._lists(lens, H, stream, keep, new_lens)
         keep_p = _array_ptr("keep", keep, dev, torch.int32, (B_, H, self.budget))
         new_p = _array_ptr("new_lens", new_lens, dev, torch.int32, (B_,))
+        if stream is not None:
+            self._lend(stream, weights, lens, keep, new_lens)
         self._call("mfa_evict_select", _cache_fns().mfa_evict_select, w_p, lens_p, B_, H, N, self.budget, self.recent,
                    keep_p, new_p, self._err, self._stream(stream))
         return keep, new_lens
@@ -708,6 +724,8 @@ class Evictor(_CacheOp):
         kd, vd, w_p, zero_p, kod, vod, wo_p, B_, H, N = self.compact._tensors(k, v, weights, zero_end, k_out, v_out, weights_out)
         lens_p = _array_ptr("lens", lens, self.device, torch.int32, (B_,))
         keep, new_lens = self._lists(lens, H, stream)
+        if stream is not None:
+            self._lend(stream, k, v, weights, lens, k_out, v_out, weights_out, zero_end)
         keep_p, new_p, s, fns = keep.data_ptr(), new_lens.data_ptr(), self._stream(stream), _cache_fns()
         self._call("mfa_evict_select", fns.mfa_evict_select, w_p, lens_p, B_, H, N, self.budget, self.recent, keep_p,
                    new_p, self._err, s)

@@ -13,7 +13,7 @@ namespace mfa {
 
 // Sequence length of batch b, clamped to the cache.
 __device__ __forceinline__ int cache_len(const int32_t* lens, int b, int N) {
-  const int n = __ldg(lens + b);
+  const int n = lens[b];
   return n < 0 ? 0 : (n > N ? N : n);
 }
 
@@ -69,7 +69,7 @@ __device__ __forceinline__ uint32_t rows_seeing(const uint32_t* seen, int words,
 
 // The error bits of node t of batch b.
 __device__ __forceinline__ uint32_t draft_errors(const int32_t* lens, const int32_t* parents, int b, int t, int T, int N) {
-  const int n = __ldg(lens + b);
+  const int n = lens[b];
   bool bad = n < 0 || n > N - T;
   if (parents != nullptr) {
     const int32_t* par = parents + static_cast<int64_t>(b) * T;
@@ -181,7 +181,9 @@ __host__ __device__ constexpr uint32_t idesc_keys(int N, bool mn_major) {
 // ---- host ----
 
 // A launch that may begin while the kernel before it in the stream ends (the
-// kernel waits for that one, griddepcontrol.wait, before it reads anything).
+// kernel waits for that one, griddepcontrol.wait, before it reads anything; what it reads then
+// may have been written while it was already there, so no load is a
+// non-coherent one).
 template <typename... P, typename... A>
 inline bool launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t cfg = {};
@@ -212,7 +214,7 @@ inline mfa_status check_cache_tensor(const mfa_tensor* t) {
 }
 
 // Whether the line's places can be counted in 32 bits (with the largest `extra`).
-inline bool line_fits(const mfa_tensor* k) { return k->B * k->H * (cdiv64(k->N, kKeys) + 4) < (int64_t(1) << 31); }
+inline bool line_fits(const mfa_tensor* k) { return k->B * k->H * (cdiv64(k->N, kKeys) + 16) < (int64_t(1) << 30); }
 
 // The checks mfa_tree_decode and mfa_key_weights share (q and the cache k
 // already checked one by one). *empty: nothing to do.

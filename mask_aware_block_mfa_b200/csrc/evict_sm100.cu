@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.x, b = blockIdx.y;
-  const int raw = __ldg(p.lens + b);
+  const int raw = p.lens[b];
   const int n = cache_len(p.lens, b, p.N);
   const int kept = min(n, p.budget);
   const int64_t row = static_cast<int64_t>(b) * p.Hkv + g;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
   uint32_t* own = s_keys + j0;
   if constexpr (SHARED) {
 #pragma unroll 8
-    for (int i = lane; i < seg; i += 32) own[i] = j0 + i < m ? order_key(__ldg(w + j0 + i)) : 0u;
+    for (int i = lane; i < seg; i += 32) own[i] = j0 + i < m ? order_key(w[j0 + i]) : 0u;
   }
   __syncthreads();
   // Lane `lane`'s keys j0 + i + 4 * lane .. + 3.
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mfa_select_kernel(const __grid
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int j = j0 + i + lane * 4 + y;
-        key[y] = j < m ? order_key(__ldg(w + j)) : 0u;
+        key[y] = j < m ? order_key(w[j]) : 0u;
       }
     }
   };
@@ -252,13 +252,13 @@ struct Moves {
   int count;
   const int32_t* idx;
   __device__ __forceinline__ Moves(const CompactParams& p, int g, int b) {
-    s = p.start ? __ldg(p.start + b) : 0;
-    count = min(max(__ldg(p.count + b), 0), p.n_idx);
+    s = p.start ? p.start[b] : 0;
+    count = min(max(p.count[b], 0), p.n_idx);
     idx = p.idx + (static_cast<int64_t>(b) * p.idx_heads + (p.idx_heads == 1 ? 0 : g)) * p.n_idx;
   }
   // The source row of entry t, or -1 when it moves nothing.
   __device__ __forceinline__ int64_t source(const CompactParams& p, int t, bool report) const {
-    const int64_t x = __ldg(idx + t);
+    const int64_t x = idx[t];
     const bool bad = x < 0 || s + x < 0 || s + x >= p.N || s + t < 0 || s + t >= p.N_out || (p.in_place && x < t);
     if (bad && report) atomicOr(p.err, MFA_DEVERR_SEL);
     return bad || (p.in_place && x == t) ? -1 : s + x;
@@ -267,7 +267,7 @@ struct Moves {
 
 __device__ __forceinline__ void zero_tail(const CompactParams& p, const Moves& mv, float* dst, int b, int64_t first, int64_t step) {
   if (!p.zero_end) return;
-  const int64_t z = min(static_cast<int64_t>(__ldg(p.zero_end + b)), p.N_out);
+  const int64_t z = min(static_cast<int64_t>(p.zero_end[b]), p.N_out);
   for (int64_t j = max(mv.s + mv.count, int64_t(0)) + first; j < z; j += step) dst[j] = 0.f;
 }
 

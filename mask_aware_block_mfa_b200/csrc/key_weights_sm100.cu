@@ -119,14 +119,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int y = 0; y < kBatch; ++y) {
       const int row = min(p.row0 + i0 + y * kStep, p.R - 1), t = p.by_g(row), h = row - t * p.G;
-      pre.q[y] = __ldg(reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]));
+      pre.q[y] = *reinterpret_cast<const uint4*>(src + h * p.qs[1] + t * p.qs[2]);
     }
   };
   auto fetch = [&]() {
     const int row = min(p.row0 + static_cast<int>(threadIdx.x), p.R - 1), t = p.by_g(row), h = w.g * p.G + row - t * p.G;
-    pre.lse = __ldg(p.lse + (static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t);
-    pre.scale = p.row_scale ? __ldg(p.row_scale + static_cast<int64_t>(w.b) * p.T + t) : 1.f;
-    pre.up = p.parents ? __ldg(p.parents + static_cast<int64_t>(w.b) * p.T + t) : 0;
+    pre.lse = p.lse[(static_cast<int64_t>(w.b) * p.Hq + h) * p.T + t];
+    pre.scale = p.row_scale ? p.row_scale[static_cast<int64_t>(w.b) * p.T + t] : 1.f;
+    pre.up = p.parents ? p.parents[static_cast<int64_t>(w.b) * p.T + t] : 0;
     fetch_q(qr);
   };
   if (threadIdx.x < kSoftThreads) fetch();
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (par && w.t1 * kKeys > w.len)
-        for (int i = threadIdx.x; i < p.T; i += kSoftThreads) sPar[i] = __ldg(par + i);
+        for (int i = threadIdx.x; i < p.T; i += kSoftThreads) sPar[i] = par[i];
       if (p.row0 == 0 && w.g == 0 && w.t0 == 0) {
         for (int t = threadIdx.x; t < (par ? p.T : 1); t += kSoftThreads) {
           const uint32_t e = draft_errors(p.lens, p.parents, w.b, t, p.T, p.N);

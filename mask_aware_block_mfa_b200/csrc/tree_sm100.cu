@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
             mbar_wait(&p_empty[n % PB], ((n / PB) - 1) & 1, s_abort);
             int* sPar = reinterpret_cast<int*>(pbuf + grp * (C::kPBytes / C::kGroups));
             uint32_t* sSeen = reinterpret_cast<uint32_t*>(sPar + MFA_TREE_MAX_NODES);  // [W][kSeenWords]
-            for (int i = tid; i < p.T; i += 128) sPar[i] = __ldg(par + i);
+            for (int i = tid; i < p.T; i += 128) sPar[i] = par[i];
             for (int i = tid; i < W * kSeenWords; i += 128) sSeen[i] = 0u;
             named_barrier(bar, 128);
             if (tid < rows && tid < W) {
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       named_barrier(bar, 128);
       if (tid < rows && tid < W) {
         const int tt = p.by_g(row0 + tid), h = w.g * p.G + row0 + tid - tt * p.G;
-        const bool dead = par && __ldg(par + tt) == -2;
+        const bool dead = par && par[tt] == -2;
         const float sum = dead ? 0.f : (part_sum + red[tid]) + (delta[tid] + alpha[tid]);
         const float m = -negM[tid];
         // Does the row see a node whose values are not finite? (Not dead: the row's way up is
@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
   if (!w.more) return;      // none of them a tile
   int parent = 0;  // of node threadIdx.x
   auto fetch_parent = [&](int b) {
-    if (p.parents && static_cast<int>(threadIdx.x) < p.T) parent = __ldg(p.parents + static_cast<int64_t>(b) * p.T + threadIdx.x);
+    if (p.parents && static_cast<int>(threadIdx.x) < p.T) parent = p.parents[static_cast<int64_t>(b) * p.T + threadIdx.x];
   };
   if (warp < 8) fetch_parent(w.b);
   int tiles = 0, loads_k = 0;  // the producer's: tiles loaded, K loads

@@ -318,6 +318,56 @@ def test_calls_on_other_streams_and_two_at_once():
         assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[1].cpu(), want[1])
 
 
+def test_a_step_on_a_named_stream_with_tensors_that_are_dropped_at_once():
+    """Every operator on a stream given by name; the inputs' last references go before the
+    work is done, and new tensors are made meanwhile on the current stream."""
+    side = torch.cuda.Stream()
+    q, k, v, lens, parents = make(22, 2, 8, 2, 7, 2000, 128, [1900, 1200], "random")
+    ref_out, ref_lse, _ = decode(q, k, v, lens, parents)
+    w_ref = B.KeyWeights()(to_gpu(q), to_gpu(k), ref_lse.cuda(), lens.cuda(), parents.cuda()).cpu()
+    keep_ref, new_ref = B.Evictor(500, 20).select(w_ref.cuda(), lens.cuda())
+    tree, kw, ev = B.TreeDecode(), B.KeyWeights(), B.Evictor(500, 20)
+    for _ in range(5):
+        args = [to_gpu(x) for x in (q, k, v, lens, parents)]
+        side.wait_stream(torch.cuda.current_stream())
+        out, lse = tree(*args, stream=side)
+        with torch.cuda.stream(side):
+            w = torch.zeros(2, 2, 2000, device="cuda")
+        kw(args[0], args[1], lse, args[3], args[4], weights_out=w, stream=side)
+        keep, new = ev(args[1], args[2], w, args[3], stream=side)
+        kept = [args[1], args[2]]
+        del args
+        junk = [torch.full((4, 2, 2000, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        side.synchronize()
+        assert torch.equal(out.cpu(), ref_out) and torch.equal(lse.cpu(), ref_lse)
+        assert torch.equal(keep, keep_ref) and torch.equal(new, new_ref)
+        rows = keep.clamp_min(0).long().cpu()[..., None].expand(2, 2, 500, 128)
+        for moved, whole in zip(kept, (k, v)):
+            assert torch.equal(moved[:, :, :500].cpu(), torch.gather(whole, 2, rows))
+        del junk
+    assert tree.status() == 0 and kw.status() == 0 and ev.status() == 0
+
+
+def test_two_graphs_with_an_object_each_replayed_in_turn():
+    q, k, v, lens, parents = make(23, 2, 8, 2, 5, 900, 128, [800, 300], "random")
+    g = [to_gpu(x) for x in (q, k, v, lens, parents)]
+    graphs = []
+    for T in (5, 2):  # the second with a smaller workspace need, from the same inputs' first rows
+        op = B.TreeDecode()
+        qq, par = g[0][:, :, :T].contiguous(), g[4][:, :T].contiguous()
+        out, lse = torch.empty_like(qq), torch.empty(2, 8, T, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            op(qq, g[1], g[2], g[3], par, out=out, lse=lse)
+        graphs.append((graph, op, out, lse, decode(q[:, :, :T], k, v, lens, parents[:, :T].contiguous())))
+    for _ in range(3):
+        for graph, op, out, lse, ref in graphs:
+            out.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out.cpu(), ref[0]) and torch.equal(lse.cpu(), ref[1]) and op.status() == 0
+
+
 def test_an_empty_batch_launches_nothing():
     q, k, v = (torch.empty(0, h, n, 64, dtype=torch.bfloat16, device="cuda") for h, n in ((4, 1), (2, 9), (2, 9)))
     lens = torch.empty(0, dtype=torch.int32, device="cuda")
