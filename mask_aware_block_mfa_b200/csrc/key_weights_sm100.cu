@@ -48,12 +48,11 @@ struct Cfg {
   static constexpr int kUnits = D == 256 ? 2 : 1;   // ring units of a K tile
   static constexpr int kUnit = (D == 64 ? 1 : 2) * kChunk;
   static constexpr int kQTile = NR * D * 2;         // NR rows x 128 B per 64 columns
-  static constexpr int kExtra = D == 256 ? 2 : D == 64 ? 4 : 3;
+  static constexpr int kExtra = D == 256 ? 4 : D == 64 ? 12 : 8;
   static constexpr int kBars = 2 * kMaxRing + 1 + 2 * kGroups + 1;
-  static constexpr int kConst = NR * 128;           // constants of the rows: 32 bytes for each row tile
-  // Bytes besides the ring (first) and Q (next): ones, constants, signs, partial sums, who sees what, barriers.
+  // Bytes besides the ring (first) and Q (next): constants and ones, signs, partial sums, who sees what, barriers.
   static constexpr int rest(int qtiles, int T, int words) {
-    return kChunk + kConst + qtiles * NR * 4 + 2 * kSoftThreads * 4 + 32 + (words > 0 ? T * 4 + T * words * 4 : 0) + 16 + kBars * 8 + 16;
+    return kChunk + qtiles * NR * 4 + 2 * kSoftThreads * 4 + 32 + (words > 0 ? T * 4 + T * words * 4 : 0) + 16 + kBars * 8 + 16;
   }
 };
 
@@ -65,9 +64,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* sQ = smem + p.ring * C::kUnit;                              // [qtiles]
-  uint8_t* sOnes = sQ + p.qtiles * C::kQTile;                          // [128 keys] 1 1 1 0 ..
-  uint8_t* sConst = sOnes + kChunk;                                    // [NR]
-  float* sSign = reinterpret_cast<float*>(sConst + C::kConst);         // [qtiles * NR] of the row's scale; 0: it is left out
+  // 128-byte rows: the rows' constants, 32 bytes for each row tile, and from byte 96 on the keys' ones, 1 1 1 0 ..
+  uint8_t* sConst = sQ + p.qtiles * C::kQTile;                         // [128]
+  float* sSign = reinterpret_cast<float*>(sConst + kChunk);            // [qtiles * NR] of the row's scale; 0: it is left out
   float* sPart = sSign + p.qtiles * NR;                                // [2][kGroups][128]
   uint32_t* sActive = reinterpret_cast<uint32_t*>(sPart + 2 * kSoftThreads);  // [8] bits: the row counts
   uint64_t* full = reinterpret_cast<uint64_t*>(sActive + 8);           // [ring]
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (++s2 == p.ring) s2 = 0;
           }
-          umma_ss(tmem + buf * NR, sdesc_sw128_lo(smem_u32(sOnes), 16), sdesc_sw128_lo(smem_u32(sConst) + rt * 32, 16), idesc, 1u);
+          umma_ss(tmem + buf * NR, sdesc_sw128_lo(smem_u32(sConst) + 96, 16), sdesc_sw128_lo(smem_u32(sConst) + rt * 32, 16), idesc, 1u);
           umma_commit(&s_full[buf]);
         }
         if (!ok) break;
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t st = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + grp * NR;
     for (int i = threadIdx.x; i < kKeys * 2; i += kSoftThreads) {
       const int r = i >> 1, u = i & 1;
-      *reinterpret_cast<uint4*>(sOnes + r * 128 + ((u ^ (r & 7)) << 4)) =
+      *reinterpret_cast<uint4*>(sConst + r * 128 + (((6 + u) ^ (r & 7)) << 4)) =
           u == 0 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
     }
     int n = 0;           // tiles of the CTA so far
