@@ -23,10 +23,10 @@
 namespace mfa {
 namespace {
 
-constexpr int kGroups = 4;                        // softmax groups of 128 threads, a TMEM buffer each
+constexpr int kGroups = 4;                        // softmax groups of 128 threads
 constexpr int kSoftThreads = kGroups * 128;
 constexpr int kThreads = kSoftThreads + 64;       // + the MMA and the TMA warp
-constexpr int kMaxRing = 8;
+constexpr int kMaxRing = 12;
 constexpr int kSmem = 232448;
 
 struct KeyWeightParams {
@@ -49,7 +49,8 @@ struct Cfg {
   static constexpr int kUnit = (D == 64 ? 1 : 2) * kChunk;
   static constexpr int kQTile = NR * D * 2;         // NR rows x 128 B per 64 columns
   static constexpr int kExtra = D == 256 ? 4 : D == 64 ? 12 : 8;
-  static constexpr int kBars = 2 * kMaxRing + 1 + 2 * kGroups + 1;
+  static constexpr int kBufs = NR <= 64 ? 2 * kGroups : kGroups;  // TMEM buffers of S, one or two for each group
+  static constexpr int kBars = 2 * kMaxRing + 1 + 2 * kBufs + 1;
   // Bytes besides the ring (first) and Q (next): constants and ones, signs, partial sums, who sees what, barriers.
   static constexpr int rest(int qtiles, int T, int words) {
     return kChunk + qtiles * NR * 4 + 2 * kSoftThreads * 4 + 32 + (words > 0 ? T * 4 + T * words * 4 : 0) + 16 + kBars * 8 + 16;
@@ -72,9 +73,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sActive + 8);           // [ring]
   uint64_t* empty = full + kMaxRing;
   uint64_t* q_full = empty + kMaxRing;
-  uint64_t* s_full = q_full + 1;         // [kGroups]
-  uint64_t* s_empty = s_full + kGroups;  // [kGroups]
-  uint64_t* drain = s_empty + kGroups;
+  uint64_t* s_full = q_full + 1;           // [kBufs]
+  uint64_t* s_empty = s_full + C::kBufs;   // [kBufs]
+  uint64_t* drain = s_empty + C::kBufs;
   volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
   int* s_minus = reinterpret_cast<int*>(s_tmem + 1);                   // a row of the pair has a negative scale
@@ -88,9 +89,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kGroups; ++i) {
+    for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 128);
+      mbar_init(&s_empty[i], 4);
     }
     mbar_init(q_full, kSoftThreads);
     mbar_init(drain, 1);
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (warp == kGroups * 4 + 1 && lane == 0) load_tile(w.t0);
   if (warp == kGroups * 4) {
-    tmem_alloc(s_tmem, kGroups * NR);
+    tmem_alloc(s_tmem, C::kBufs * NR);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kGroups * 4) {
     // =================== S^T = K Q^T ===================
-    // Item i = tile * qtiles + row tile goes to buffer and group i % 4.
+    // Item i = tile * qtiles + row tile goes to buffer i % kBufs and group i % 4.
     constexpr uint32_t idesc = idesc_keys(NR, false);
     const uint32_t ring = smem_u32(smem), q_addr = smem_u32(sQ);
     bool ok = true;
@@ -193,9 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         for (int rt = 0; rt < p.qtiles; ++rt, ++item) {
-          const int buf = item % kGroups;
-          if (item >= kGroups)
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_empty[buf], (item / kGroups - 1) & 1, s_abort));
+          const int buf = item % C::kBufs;
+          if (item >= C::kBufs)
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_empty[buf], (item / C::kBufs - 1) & 1, s_abort));
           if (!ok) break;
           tc_fence_after();
           s2 = slot;
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // then fails at once): the barriers below need all threads.
     const int grp = warp >> 2, tid = threadIdx.x & 127;
     const int rt = grp & (p.qtiles - 1), nn = kGroups / p.qtiles;  // the group's row tile; tiles in flight
-    const uint32_t st = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + grp * NR;
+    const uint32_t tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     for (int i = threadIdx.x; i < kKeys * 2; i += kSoftThreads) {
       const int r = i >> 1, u = i & 1;
       *reinterpret_cast<uint4*>(sConst + r * 128 + (((6 + u) ^ (r & 7)) << 4)) =
@@ -313,7 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float old = 0.f;
         if (mine && add) old = p.w_in[out0 + j];
         uint64_t acc[2] = {0ull, 0ull};
-        mbar_wait(&s_full[grp], k & 1, s_abort);
+        constexpr int kEach = C::kBufs / kGroups;
+        const int buf = grp + k % kEach * kGroups;
+        const uint32_t st = tm + buf * NR;
+        mbar_wait(&s_full[buf], (k / kEach) & 1, s_abort);
         tc_fence_after();
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
         if (t * kKeys + kKeys <= w.len && !minus) {
@@ -351,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc[0] = f2_pack(sum, 0.f);
         }
         tc_fence_before();
-        mbar_arrive(&s_empty[grp]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[buf]);
         const uint64_t both = f2_add(acc[0], acc[1]);
         float lo, hi;
         f2_unpack(both, lo, hi);
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kGroups * 4) {
     tc_fence_after();
-    tmem_dealloc(tmem, kGroups * NR);
+    tmem_dealloc(tmem, C::kBufs * NR);
   }
 }
 
