@@ -242,10 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int n = 0;           // tiles of the CTA so far
     int k = 0;           // of them the group's
-    bool begun = false;
     do {
-      if (begun) fetch();
-      begun = true;
       const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
       // ---- the pair's rows (all of the last pair's S and sums are done) ----
       // Rows that count for nothing, whatever they hold, become Q = 0 with a constant that
@@ -347,12 +344,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tmem_ld_32x32b_x32(st + c, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < X; ++i) {
-              const float e = ex2_approx(__uint_as_float(x[i]) * p.scale_log2);
-              sum = fmaf(see >> i & 1 ? e : 0.f, sSign[rt * NR + c + i], sum);
+            for (int i = 0; i < X; ++i) x[i] = see >> i & 1 ? x[i] : 0xff800000u;
+            if (minus) {
+#pragma unroll
+              for (int i = 0; i < X; ++i) sum = fmaf(ex2_approx(__uint_as_float(x[i]) * p.scale_log2), sSign[rt * NR + c + i], sum);
+            } else {
+#pragma unroll
+              for (int i = 0; i < X; i += 2) {
+                float a, b;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2), a, b);
+                acc[(i >> 1) & 1] = f2_add(acc[(i >> 1) & 1], f2_pack(ex2_approx(a), ex2_approx(b)));
+              }
             }
           }
-          acc[0] = f2_pack(sum, 0.f);
+          acc[0] = f2_add(acc[0], f2_pack(sum, 0.f));
         }
         tc_fence_before();
         __syncwarp();
@@ -373,8 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++k;
       }
       if (threadIdx.x == 0) *s_minus = 0;
+      if (w.next(ln)) fetch();  // the next pair's
       named_barrier(1, kSoftThreads);  // every sum of the pair is done
-    } while (w.next(ln));
+    } while (w.more);
     if (*s_abort && threadIdx.x == 0) atomicOr(p.err, MFA_DEVERR_TIMEOUT);
   }
   __syncthreads();
