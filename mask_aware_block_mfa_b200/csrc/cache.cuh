@@ -178,6 +178,16 @@ __host__ __device__ constexpr uint32_t idesc_keys(int N, bool mn_major) {
   return idesc_bf16_f32(128, N, mn_major) | (mn_major ? 1u << 15 : 0u);
 }
 
+// Waits of a whole warp for one barrier, and for two at once (the lanes share them out: a
+// wait that is over still takes about 130 cycles beside 16 busy warps).
+__device__ __forceinline__ bool warp_wait(uint64_t* a, uint32_t pa, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(a, pa, abort)) != 0;
+}
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* abort) {
+  const bool odd = threadIdx.x & 1;
+  return __all_sync(0xffffffffu, mbar_wait(odd ? b : a, odd ? pb : pa, abort)) != 0;
+}
+
 // ---- host ----
 
 // A launch that may begin while the kernel before it in the stream ends (the

@@ -184,19 +184,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     do {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(q_full, seg & 1, s_abort));
       for (int t = w.t0; t < w.t1 && ok; ++t) {
-        int s2 = slot, r2 = round;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[s2], r2 & 1, s_abort));
-          if (++s2 == p.ring) {
-            s2 = 0;
-            ++r2;
-          }
-        }
         for (int rt = 0; rt < p.qtiles; ++rt, ++item) {
+          // The K units, and the buffer as its last sums were read (at once for the first uses: their phase is before the first).
           const int buf = item % C::kBufs;
-          if (item >= C::kBufs)
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_empty[buf], (item / C::kBufs - 1) & 1, s_abort));
+          const uint32_t free = (item / C::kBufs + 1) & 1;
+          int s2 = slot, r2 = round;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            ok = ok && (u == 0 ? warp_wait2(&full[s2], r2 & 1, &s_empty[buf], free, s_abort) : warp_wait(&full[s2], r2 & 1, s_abort));
+            if (++s2 == p.ring) {
+              s2 = 0;
+              ++r2;
+            }
+          }
           if (!ok) break;
           tc_fence_after();
           s2 = slot;
@@ -211,16 +211,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (++s2 == p.ring) s2 = 0;
           }
           umma_ss(tmem + buf * NR, sdesc_sw128_lo(smem_u32(sConst) + 96, 16), sdesc_sw128_lo(smem_u32(sConst) + rt * 32, 16), idesc, 1u);
-          umma_commit(&s_full[buf]);
+          umma_commit(&s_full[buf]);  // (the tile's last group hands the K units back)
         }
         if (!ok) break;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          umma_commit(&empty[slot]);
-          if (++slot == p.ring) {
-            slot = 0;
-            ++round;
-          }
+        slot += U;
+        if (slot >= p.ring) {
+          slot -= p.ring;
+          ++round;
         }
       }
       ++seg;
@@ -316,6 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t st = tm + buf * NR;
         mbar_wait(&s_full[buf], (k / kEach) & 1, s_abort);
         tc_fence_after();
+        // S of the tile's last row tile is done, and so those before it: K may be overwritten.
+        if (rt == p.qtiles - 1 && tid < U) mbar_arrive(&empty[(n * U + tid) % p.ring]);
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
         if (t * kKeys + kKeys <= w.len && !minus) {
 #pragma unroll
