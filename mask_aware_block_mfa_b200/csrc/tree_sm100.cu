@@ -86,7 +86,7 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const CUtensorMap* t
 // ---------------------------------------------------------------------------
 template <int D, int NR>
 struct Cfg {
-  static constexpr int kCols = NR < 32 ? NR : 32;       // rows (registers) per softmax thread
+  static constexpr int kCols = 16;                      // rows (registers) per softmax thread
   static constexpr int kGroups = NR / kCols;            // groups of 4 softmax warps
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kThreads = (kSoftWarps + 4) * 32;  // + S, P.V, TMA of K and V, TMA of Q
