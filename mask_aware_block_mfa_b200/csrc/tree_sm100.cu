@@ -393,18 +393,24 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
     do {
       for (int t = w.t0; t < w.t1 && ok; ++t, ++n) {
         const uint32_t first = static_cast<uint32_t>(n) * U;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_full[n % PB], (n / PB) & 1, s_abort)))) break;
         const uint32_t pb = sdesc_sw128_lo(smem_u32(smem + C::kP) + (n % PB) * C::kPBytes, kChunk);
-        if (t * kKeys + kKeys > w.len) {
+        const bool draft = t * kKeys + kKeys > w.len;
+        int steps = kKeys / 16;
+        // V is cleaned while P is computed, but in a pair's first tile, whose P also says that
+        // the last epilogue has read sBad.
+        if (!draft || t == w.t0) ok = warp_wait(&p_full[n % PB], (n / PB) & 1, s_abort);
+        if (ok && (draft || t == w.t0)) {
+          uint8_t* unit[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[RK + (first + u) % RV], ((first + u) / RV) & 1, s_abort));
-          if (!ok) break;
+          for (int u = 0; u < U; ++u) {
+            const uint32_t slot = RK + (first + u) % RV;
+            unit[u] = smem + C::kRing0 + slot * C::kUnit;
+            ok = ok && warp_wait(&full[slot], ((first + u) / RV) & 1, s_abort);
+          }
+          if (ok) steps = clean_values<D, U>(p, w, t, lane, sBad, sBadMin, unit);
+          if (ok && t != w.t0) ok = warp_wait(&p_full[n % PB], (n / PB) & 1, s_abort);
         }
-        uint8_t* unit[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) unit[u] = smem + C::kRing0 + (RK + (first + u) % RV) * C::kUnit;
-        const int steps = clean_values<D, U>(p, w, t, lane, sBad, sBadMin, unit);
+        if (!ok) break;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const uint32_t slot = RK + (first + u) % RV;
