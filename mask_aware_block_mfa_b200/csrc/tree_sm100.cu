@@ -48,6 +48,7 @@ struct TreeParams {
   const int32_t *lens, *parents;
   __nv_bfloat16* out;
   float *lse, *o_part, *ml_part;  // parts: [rtiles * groups][2][NR][D] and [..][NR][2] (m, l)
+  int2* cut;                      // [rtiles][B][Hkv] a pair's first CTA, and how many it has
   uint32_t* err;
 };
 
@@ -70,6 +71,12 @@ struct RowTile {
   }
   __device__ __forceinline__ int last_node(const TreeParams& p) const { return p.parts == 1 ? min(node0 + p.tile_t, p.T) - 1 : node0; }
 };
+
+// By the CTA that has pair w's first tile: the CTAs that share the pair, for the merge. Those
+// behind this one each take `per` places of it.
+__device__ __forceinline__ void note_cut(const TreeParams& p, const Walk& w, int rt, int cta, int per) {
+  p.cut[(static_cast<int64_t>(rt) * p.B + w.b) * p.Hkv + w.g] = make_int2(cta, 1 + (w.nt - w.t1 + per - 1) / per);
+}
 
 // Q of a row tile by TMA: its boxes of 64 columns.
 template <int D, int NR>
@@ -285,6 +292,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   if (start.b < 0) return;  // more CTAs than places
   Walk w(ln, start, p.groups);
   if (!w.more) return;      // none of them a tile
+  const int per = places_per_cta(start.total, p.groups);
   const uint32_t ring = smem_u32(smem + C::kRing0);
   const int tile_fill = p.parts == 1 ? p.tile_t * p.G : NR;  // rows of Q's box
   // The TMA producer's state: K (and V) units issued; slots ever loaded, parity of the last load.
@@ -463,6 +471,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         negM[tid] = 0.f;
         sSet[col0 + tid] = 0;
       }
+      if (threadIdx.x == 0 && w.t0 == 0 && p.groups > 1) note_cut(p, w, rt, cta, per);
       if (rt == 0 && w.g == 0 && w.t0 == 0) {
         for (int t = threadIdx.x; t < (par ? p.T : 1); t += C::kSoftWarps * 32) {
           const uint32_t e = draft_errors(p.lens, p.parents, w.b, t, p.T, p.N);
@@ -792,6 +801,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
   if (start.b < 0) return;  // more CTAs than places
   Walk w(ln, start, p.groups);
   if (!w.more) return;      // none of them a tile
+  const int per = places_per_cta(start.total, p.groups);
   int parent = 0;  // of node threadIdx.x
   auto fetch_parent = [&](int b) {
     if (p.parents && static_cast<int>(threadIdx.x) < p.T) parent = p.parents[static_cast<int64_t>(b) * p.T + threadIdx.x];
@@ -937,6 +947,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
     do {
       const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
       if (par) sPar[threadIdx.x] = static_cast<int16_t>(parent < -2 || parent > INT16_MAX ? -3 : parent);
+      if (threadIdx.x == 0 && w.t0 == 0 && p.groups > 1) note_cut(p, w, rt, cta, per);
       if (rt == 0 && w.g == 0 && w.t0 == 0) {
         for (int t = threadIdx.x; t < (par ? p.T : 1); t += 256) {
           const uint32_t e = draft_errors(p.lens, p.parents, w.b, t, p.T, p.N);
@@ -1141,7 +1152,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
 
-template <int D, int NR, int EXTRA, bool SPLIT>
+template <int D, int NR, bool SPLIT>
 __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_constant__ TreeParams p) {
   constexpr int E = D / 32, WS = SPLIT ? kMergeWarps : 1;
   __shared__ float so[SPLIT ? kMergeWarps : 1][D];
@@ -1153,22 +1164,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
   const RowTile tile(p, rt, NR);
   if (r >= tile.rows) return;  // (SPLIT: the whole block)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // The CTAs that met the pair.
-  const Line ln{p.lens, p.B, p.Hkv, p.N, tile.last_node(p), EXTRA};
-  int before = 0, total = 0;
-  for (int x = lane; x < p.B; x += 32) {
-    const int n = ln.tiles(ln.len(x)) + ln.extra;
-    total += n;
-    if (x < b) before += n;
-  }
-  total = __reduce_add_sync(0xffffffffu, total) * p.Hkv;
-  before = __reduce_add_sync(0xffffffffu, before);
-  const int nt = ln.tiles(ln.len(b));
-  const int base = before * p.Hkv + g * (nt + ln.extra) + ln.extra;  // of its first tile
-  const int per = places_per_cta(total, p.groups);
-  const int c0 = base / per, c1 = (base + nt - 1) / per;
-  if (c0 == c1) return;  // written by its only CTA
-  const int ns = c1 - c0 + 1;
+  const int2 cut = p.cut[static_cast<int64_t>(rt) * p.B * p.Hkv + blockIdx.x];
+  const int c0 = cut.x, ns = cut.y;
+  if (ns == 1) return;  // written by its only CTA
   // Part s of the row: the first CTA met the pair's first tile (its second slot), the
   // others begin inside it.
   auto at = [&](int s) {
@@ -1256,11 +1254,15 @@ TreePlan plan_tree(int64_t T, int64_t G, int64_t D) {
   return pl;
 }
 
-// Bytes of the parts' outputs and of all (one CTA per row tile: no pair is cut).
-size_t part_bytes(const TreePlan& pl, int64_t D, size_t* o_bytes) {
-  const size_t rows = pl.groups == 1 ? 0 : static_cast<size_t>(pl.rtiles) * pl.groups * 2 * pl.nr;
-  *o_bytes = align256(rows * D * 4);
-  return *o_bytes + align256(rows * 2 * 4) + 256;
+// Bytes of the parts' outputs, of their (m, l) and of all (one CTA per row tile: no pair is cut).
+struct TreeSpace {
+  size_t o, ml, all;
+};
+TreeSpace tree_space(const TreePlan& pl, int64_t D, int64_t pairs) {
+  if (pl.groups == 1) return {0, 0, 256};
+  const size_t rows = static_cast<size_t>(pl.rtiles) * pl.groups * 2 * pl.nr;
+  const size_t o = align256(rows * D * 4), ml = align256(rows * 2 * 4);
+  return {o, ml, o + ml + align256(static_cast<size_t>(pl.rtiles) * pairs * sizeof(int2))};
 }
 
 // The tensor map of q: boxes of 64 columns x the heads of a group x the nodes of a row tile.
@@ -1277,7 +1279,7 @@ bool map_queries(CUtensorMap* map, const mfa_tensor* q, const TreePlan& pl, int6
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NR, int EXTRA, typename K>
+template <int D, int NR, typename K>
 mfa_status launch_tree(K kernel, int threads, int bytes, std::atomic<uint64_t>& attr_devs, const CUtensorMap& mq, const CUtensorMap& mk,
                        const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), bytes, attr_devs)) return MFA_ERR_CUDA;
@@ -1285,9 +1287,9 @@ mfa_status launch_tree(K kernel, int threads, int bytes, std::atomic<uint64_t>& 
   if (p.groups > 1) {
     const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
     const int rows = p.parts > 1 ? NR : p.tile_t * p.G;  // of a tile
-    const bool split = pairs * p.R <= 1024;
+    const bool split = pairs * p.R <= 1024;  // about one wave of blocks (256 and 4096 measured 10 to 20% slower around it)
     const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>((split ? rows : cdiv64(rows, kMergeWarps)) * p.rtiles));
-    if (!launch_after(split ? mfa_tree_merge<D, NR, EXTRA, true> : mfa_tree_merge<D, NR, EXTRA, false>, grid, kMergeWarps * 32, 0, s, p))
+    if (!launch_after(split ? mfa_tree_merge<D, NR, true> : mfa_tree_merge<D, NR, false>, grid, kMergeWarps * 32, 0, s, p))
       return MFA_ERR_CUDA;
   }
   return MFA_OK;
@@ -1297,14 +1299,14 @@ template <int D, int NR>
 mfa_status launch_keys(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
   using C = Cfg<D, NR>;
   static std::atomic<uint64_t> attr_devs{0};
-  return launch_tree<D, NR, C::kExtra>(mfa_tree_kernel<D, NR>, C::kThreads, C::kBytes, attr_devs, mq, mk, mv, p, s);
+  return launch_tree<D, NR>(mfa_tree_kernel<D, NR>, C::kThreads, C::kBytes, attr_devs, mq, mk, mv, p, s);
 }
 
 template <int D>
 mfa_status launch_rows(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, cudaStream_t s) {
   using C = RowCfg<D>;
   static std::atomic<uint64_t> attr_devs{0};
-  return launch_tree<D, 128, C::kExtra>(mfa_tree_rows_kernel<D>, C::kThreads, C::kBytes, attr_devs, mq, mk, mv, p, s);
+  return launch_tree<D, 128>(mfa_tree_rows_kernel<D>, C::kThreads, C::kBytes, attr_devs, mq, mk, mv, p, s);
 }
 
 template <int D>
@@ -1326,8 +1328,7 @@ extern "C" size_t mfa_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t
   using namespace mfa;
   if (B < 0 || Hq <= 0 || Hkv <= 0 || T < 0 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
   if (B == 0 || T == 0) return 256;
-  size_t o_bytes;
-  return part_bytes(plan_tree(T, Hq / Hkv, D), D, &o_bytes);
+  return tree_space(plan_tree(T, Hq / Hkv, D), D, static_cast<int64_t>(B) * Hkv).all;
 }
 
 extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, const mfa_tensor* v,
@@ -1345,9 +1346,8 @@ extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, 
   if (empty) return MFA_OK;
   const int64_t R = q->N * (q->H / k->H);
   const TreePlan pl = plan_tree(q->N, q->H / k->H, q->D);
-  size_t o_bytes;
-  const size_t need = part_bytes(pl, q->D, &o_bytes);
-  if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+  const TreeSpace sp = tree_space(pl, q->D, k->B * k->H);
+  if (!workspace || workspace_bytes < sp.all || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
     return MFA_ERR_INVALID_ARG;
   CUtensorMap mq, mk, mv;
   if (!map_queries(&mq, q, pl, q->H / k->H) || !map_keys(&mk, k) || !map_keys(&mv, v)) return MFA_ERR_CUDA;
@@ -1362,7 +1362,8 @@ extern "C" mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, 
   p.lens = lens; p.parents = parents;
   p.out = static_cast<__nv_bfloat16*>(out->data); p.lse = lse; p.err = dev_err;
   p.o_part = static_cast<float*>(workspace);
-  p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + o_bytes);
+  p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.o);
+  p.cut = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + sp.o + sp.ml);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (q->D == 64) return launch_tree_rows<64>(pl.nr, mq, mk, mv, p, s);
   if (q->D == 128) return launch_tree_rows<128>(pl.nr, mq, mk, mv, p, s);
