@@ -326,30 +326,31 @@ __global__ void __launch_bounds__(kMoveThreads) mfa_compact_kernel(const __grid_
 // before it is overwritten; the next chunk's rows lie behind all that this
 // one writes, so they are loaded before, and the list one chunk earlier still. Blocks share
 // nothing: each moves its own slice of the columns of one head's K or V, one more block the weights.
-// (64 lists of 8192 of 32768 rows of 128: 102 us, 5.3 TB/s; with slices of 8 or 16 units, or
-// 4 entries, 104 to 157 us.)
+// Entries per thread and chunk (BATCH): 8 for long lists (64 lists of 8192 of 32768 rows of
+// 128: 102 us, 5.3 TB/s; with 4, or slices of 8 or 16 units, 104 to 157 us), 2 where
+// that takes the whole list in a chunk (6 rows of 64 heads: 3.5 us against 9.1, as more blocks fit an SM).
 constexpr int kSlice = 4;   // 16-byte units of a row per block
-constexpr int kBatch = 8;   // entries per thread and chunk
+constexpr int kShort = 2 * (kMoveThreads / kSlice);
 
 // Moves a block's list: the thread's entries are first, first + step, ...; its rows' data are at[row * pitch].
-template <typename T>
+template <int BATCH, typename T>
 __device__ __forceinline__ void move_in_order(const CompactParams& p, const Moves& mv, int first, int step, T* at, int64_t pitch, bool mine,
                                               bool report) {
-  const int count = mv.count, chunk = kBatch * step;
-  int id[2][kBatch];
-  T x[2][kBatch];
+  const int count = mv.count, chunk = BATCH * step;
+  int id[2][BATCH];
+  T x[2][BATCH];
   unsigned have[2] = {0u, 0u};
-  auto list = [&](int base, int (&v)[kBatch]) {
+  auto list = [&](int base, int (&v)[BATCH]) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       const int t = base + first + i * step;
       v[i] = t < count ? mv.idx[t] : 0;
     }
   };
-  auto fetch = [&](int base, const int (&v)[kBatch], T (&y)[kBatch]) {
+  auto fetch = [&](int base, const int (&v)[BATCH], T (&y)[BATCH]) {
     unsigned moves = 0, bad = 0;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       const int t = base + first + i * step;
       const int64_t r = mv.s + v[i], to = mv.s + t;
       const bool in = t < count, good = v[i] >= t && r >= 0 && r < p.N && to >= 0 && to < p.N_out;
@@ -357,14 +358,14 @@ __device__ __forceinline__ void move_in_order(const CompactParams& p, const Move
       moves |= (mine && in && good && v[i] != t ? 1u : 0u) << i;
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < BATCH; ++i)
       if (moves >> i & 1) y[i] = at[(mv.s + v[i]) * pitch];
     if (bad && report) atomicOr(p.err, MFA_DEVERR_SEL);
     return moves;
   };
-  auto put = [&](int base, const T (&y)[kBatch], unsigned moves) {
+  auto put = [&](int base, const T (&y)[BATCH], unsigned moves) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < BATCH; ++i)
       if (moves >> i & 1) at[(mv.s + base + first + i * step) * pitch] = y[i];
   };
   list(0, id[0]);
@@ -382,6 +383,7 @@ __device__ __forceinline__ void move_in_order(const CompactParams& p, const Move
   }
 }
 
+template <int BATCH>
 __global__ void __launch_bounds__(kMoveThreads) mfa_compact_in_place_kernel(const __grid_constant__ CompactParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -393,10 +395,10 @@ __global__ void __launch_bounds__(kMoveThreads) mfa_compact_in_place_kernel(cons
     const int slice = blockIdx.x - (isv ? slices : 0);
     const int u = slice * kSlice + threadIdx.x % kSlice;
     uint4* at = isv ? p.v_out + b * p.vs[0] + g * p.vs[1] + u : p.k_out + b * p.ks[0] + g * p.ks[1] + u;
-    move_in_order(p, mv, static_cast<int>(threadIdx.x) / kSlice, kMoveThreads / kSlice, at, isv ? p.vs[2] : p.ks[2], u < p.units, blockIdx.x == 0);
+    move_in_order<BATCH>(p, mv, static_cast<int>(threadIdx.x) / kSlice, kMoveThreads / kSlice, at, isv ? p.vs[2] : p.ks[2], u < p.units, blockIdx.x == 0);
   } else {
     float* at = p.w_out + (static_cast<int64_t>(b) * p.Hkv + g) * p.N;
-    move_in_order(p, mv, static_cast<int>(threadIdx.x), kMoveThreads, at, int64_t(1), true, false);
+    move_in_order<BATCH>(p, mv, static_cast<int>(threadIdx.x), kMoveThreads, at, int64_t(1), true, false);
     __syncthreads();
     zero_tail(p, mv, at, b, threadIdx.x, kMoveThreads);
   }
@@ -501,7 +503,8 @@ extern "C" mfa_status mfa_cache_compact(const mfa_tensor* k, const mfa_tensor* v
   if (in_place) {
     const int slices = (p.units + kSlice - 1) / kSlice;
     const dim3 grid(2 * slices + (weights ? 1 : 0), p.Hkv, p.B);
-    return launch_after(mfa_compact_in_place_kernel, grid, kMoveThreads, 0, cs, p) ? MFA_OK : MFA_ERR_CUDA;
+    return launch_after(n_idx <= kShort ? mfa_compact_in_place_kernel<2> : mfa_compact_in_place_kernel<8>, grid, kMoveThreads, 0, cs, p)
+               ? MFA_OK : MFA_ERR_CUDA;
   }
   const dim3 grid(static_cast<unsigned>(n_idx > 0 ? cdiv64(n_idx, kApartRows) : 1), p.Hkv, p.B);
   auto* kernel = p.units == 8 ? mfa_compact_kernel<8> : p.units == 16 ? mfa_compact_kernel<16>
