@@ -3,26 +3,31 @@
 // out[b, h, t] = sum_j p_j v_j with p = softmax over the keys j the row sees of
 // q . k_j / sqrt(D): every key before lens[b], and of the drafted ones behind
 // it node t itself and its ancestors. The R = T * G rows of a key/value head
-// (row t * G + h') read the same keys, so K and V are read once for up to 128
-// rows; with more rows the CTAs of the row tiles walk the same keys side by
-// side and share them in L2. Up to about 200 rows the work is bound by HBM.
+// (row t * G + h') read the same keys, so K and V are read once for a tile of
+// up to 128 rows; with more rows the CTAs of the row tiles walk the same keys side by
+// side and share them in L2. Bound: HBM up to about 100 rows (8 x 8 lists of
+// 31,000 keys of 256 columns, 16 rows each: 297 us, 6.9 TB/s), above them the softmax
+// and its exchange with the products (8 x 8 lists of 25,000 keys of 128, 256
+// rows each: 237 us, 715 TFLOP/s; 288 us at the 1.37 GHz of the power limit).
 //
-// The products are transposed, S^T = K Q^T and O^T += V^T P^T, so that the 128
-// rows of a tcgen05 MMA are 128 keys (or D columns) and its N is the number of
-// query rows, 16 to 128: a decoded token pays for 16 rows, not 128, and a
-// thread holds the scores of ONE key for all rows. The softmax then has no
-// work along a thread's registers: the running maximum of a row is shared by
-// the threads through shared memory and only checked (one comparison chain
-// and one barrier vote per 128 keys); it moves when a score exceeds it by
-// more than 8 (2^8 fits every type here), and the sums stay per thread until
-// the end. P^T goes to shared memory as bf16 (the tensor core's input type; half a step
-// of each weight), where it lies as the MMA's B operand wants it.
+// Up to 64 rows (and for D = 256) the products are transposed, S^T = K Q^T and
+// O^T += V^T P^T, so that the 128 rows of a tcgen05 MMA are 128 keys (or D
+// columns) and its N is the number of query rows, 16, 32 or 64: a decoded token
+// pays for 16 rows, not 128, and a thread holds the scores of ONE key for 16 rows. The
+// running maximum of a row is shared by the threads through shared memory and
+// only checked (one comparison chain and one vote per 128 keys, beside the
+// exponentials); it moves when a score exceeds it by more than 8 (2^8 fits
+// every type here), and the sums stay per thread until the end. P^T goes to
+// shared memory as bf16 (the tensor core's input type; half a step of each
+// weight), where it lies as the MMA's B operand wants it. More rows: see
+// mfa_tree_rows_kernel.
 //
 // The tiles (128 keys) of all (batch, head) pairs are laid end to end and cut
 // into equal ranges, one per CTA, from the lengths on the device: the grid
 // does not depend on them. A pair met by one CTA is written directly; of a
 // pair cut between CTAs each writes an unnormalised part (m, l, o), and a
-// dependent launch merges them in a fixed order.
+// dependent launch merges them in a fixed order. The next pair's Q, K and V are
+// loaded, and its first S computed, while a pair ends.
 #include <cfloat>
 #include <climits>
 #include <cmath>
