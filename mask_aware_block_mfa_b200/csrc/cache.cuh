@@ -188,6 +188,18 @@ __device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b
   return __all_sync(0xffffffffu, mbar_wait(odd ? b : a, odd ? pb : pa, abort)) != 0;
 }
 
+// A named barrier that tells whether x holds in any of its threads.
+__device__ __forceinline__ bool vote_or(uint32_t id, uint32_t threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(x ? 1u : 0u), "r"(id), "r"(threads) : "memory");
+  return r != 0;
+}
+
 // ---- host ----
 
 // A launch that may begin while the kernel before it in the stream ends (the

@@ -79,8 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = s_empty + C::kBufs;
   volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
-  int* s_minus = reinterpret_cast<int*>(s_tmem + 1);                   // a row of the pair has a negative scale
-  int* sPar = s_minus + 1;                                             // [T] the tree
+  int* sPar = reinterpret_cast<int*>(s_tmem + 1);                      // [T] the tree
   uint32_t* sSeen = reinterpret_cast<uint32_t*>(sPar + p.T);           // [T][words] the nodes each one sees
 
   asm volatile("griddepcontrol.launch_dependents;");
@@ -97,7 +96,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_full, kSoftThreads);
     mbar_init(drain, 1);
     *s_abort = 0;
-    *s_minus = 0;
     fence_mbarrier_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -242,16 +240,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0;           // of them the group's
     do {
       const int32_t* par = p.parents ? p.parents + static_cast<int64_t>(w.b) * p.T : nullptr;
+      float sign;  // of the thread's row's scale
       // ---- the pair's rows (all of the last pair's S and sums are done) ----
       // Rows that count for nothing, whatever they hold, become Q = 0 with a constant that
       // no exponential survives.
       {
         const int i = threadIdx.x, r = i % NR, q = i / NR;
         const bool real = i < p.qtiles * NR;
-        float c = -1e30f, sign = 0.f;
+        float c = -1e30f;
+        sign = 0.f;
         if (real && p.row0 + i < p.R && pre.scale != 0.f && pre.lse != -INFINITY && pre.up != -2) {
           sign = pre.scale < 0.f ? -1.f : 1.f;
-          if (pre.scale < 0.f) *s_minus = 1;
           c = (log2f(fabsf(pre.scale)) - pre.lse * 1.4426950408889634f) * p.unscale;  // in the scores' unit
         }
         const unsigned active = __ballot_sync(0xffffffffu, sign != 0.f);
@@ -278,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (e) atomicOr(p.err, e);
         }
       }
-      named_barrier(1, kSoftThreads);
+      const bool minus = vote_or(1, kSoftThreads, sign < 0.f);  // a row of the pair has a negative scale
       if (par && w.t1 * kKeys > w.len) {
         for (int t = threadIdx.x; t < p.T; t += kSoftThreads) {
           for (int x = 0; x < p.words; ++x) sSeen[t * p.words + x] = 0u;
@@ -298,7 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(q_full);
       named_barrier(1, kSoftThreads);  // sSeen is complete
-      const bool minus = *s_minus != 0;
 
       const int64_t out0 = (static_cast<int64_t>(w.b) * p.Hkv + w.g) * p.N;
       const int end = min(w.len + p.T, p.N);
@@ -377,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mine) p.w_out[out0 + j] = add ? fmaf(p.decay, old, sum) : sum;
         ++k;
       }
-      if (threadIdx.x == 0) *s_minus = 0;
       if (w.next(ln)) fetch();  // the next pair's
       named_barrier(1, kSoftThreads);  // every sum of the pair is done
     } while (w.more);

@@ -123,16 +123,6 @@ struct Cfg {
   static_assert(kTmem <= 512, "TMEM columns");
 };
 
-__device__ __forceinline__ bool vote_or(uint32_t id, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r) : "r"(x ? 1u : 0u), "r"(id) : "memory");
-  return r != 0;
-}
 __device__ __forceinline__ float warp_max(float x) {  // NaN is ignored unless all are
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
@@ -565,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
               alpha[tid] = set ? ex2_approx(-d) : 1.f;  // a row without a maximum has no sums yet
               moved = set && d != 0.f;
             }
-            if (vote_or(bar, moved)) {
+            if (vote_or(bar, 128, moved)) {
 #pragma unroll
               for (int c = 0; c < W / 2; ++c) {
                 float a, b;

@@ -469,6 +469,24 @@ def test_key_weights_leave_out_what_rows_of_scale_zero_hold():
     assert torch.equal(kw(q.cuda(), k.cuda(), lse.cuda(), lens.cuda(), parents.cuda(), row.cuda(), old, 0.0), ref)
 
 
+@pytest.mark.parametrize("D,T", [(64, 3), (128, 5), (256, 20)])
+def test_key_weights_with_scales_of_both_signs_over_many_short_pairs(D, T):
+    """Several pairs of one or two tiles for each block, every second batch's with a negative scale."""
+    Bz, Hkv, N = 160, 6, 200
+    lens = [(37 * b) % (N - T + 1) for b in range(Bz)]
+    q, k, v, lens, _ = make(D, Bz, Hkv, Hkv, T, N, D, lens)
+    lse = torch.from_numpy(OT.tree_attention(q, k, v, lens)[1]).float()
+    row = torch.rand(Bz, T, generator=torch.Generator().manual_seed(5)) + 0.5
+    row[::2, T // 2] *= -1.0
+    ref = OT.key_weights(q, k, lse, lens, None, row)
+    tol = weights_tolerance(q, k, lse, lens, None, row, None, 1.0, ref)
+    kw = B.KeyWeights()
+    runs = [kw(q.cuda(), k.cuda(), lse.cuda(), lens.cuda(), None, row.cuda()) for _ in range(10)]
+    assert kw.status() == 0
+    assert (np.abs(runs[0].cpu().double().numpy() - ref) <= tol).all()
+    assert all(torch.equal(r, runs[0]) for r in runs)
+
+
 # ---- eviction ----
 
 def weights_like(g, *shape):
