@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // S of the tile's last row tile is done, and so those before it: K may be overwritten.
         if (rt == p.qtiles - 1 && tid < U) mbar_arrive(&empty[(n * U + tid) % p.ring]);
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-        if (t * kKeys + kKeys <= w.len && !minus) {
+        bool plain = t * kKeys + kKeys <= w.len && !minus;
+        if (plain) {
 #pragma unroll
           for (int c = 0; c < NR; c += X) {
             uint32_t x[X];
@@ -329,9 +330,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc[(i >> 1) & 1] = f2_add(acc[(i >> 1) & 1], f2_pack(ex2_approx(a), ex2_approx(b)));
             }
           }
-        } else {
-          // Negative scales, or drafted keys: a thread leaves out the rows that do not see its own.
+          // An infinity in a key makes the rows left out NaN (their Q is 0): do those keys with the rows that count.
+          float a, b;
+          f2_unpack(f2_add(acc[0], acc[1]), a, b);
+          plain = !__any_sync(0xffffffffu, isnan(a + b));
+        }
+        if (!plain) {
+          // Negative scales, drafted keys or infinities: a thread leaves out the rows that do not see its key.
           float sum = 0.f;
+          acc[0] = acc[1] = 0ull;
 #pragma unroll 1
           for (int c = 0; c < NR; c += X) {
             const int first = p.row0 + rt * NR + c;

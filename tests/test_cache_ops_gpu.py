@@ -487,6 +487,29 @@ def test_key_weights_with_scales_of_both_signs_over_many_short_pairs(D, T):
     assert all(torch.equal(r, runs[0]) for r in runs)
 
 
+@pytest.mark.parametrize("D,G,T", [(64, 1, 1), (128, 2, 3), (64, 4, 10), (128, 4, 40), (256, 4, 30)])
+@pytest.mark.parametrize("scaled", [False, True])
+def test_key_weights_of_keys_that_score_minus_infinity(D, G, T, scaled):
+    """An infinite key that every row scores -inf gets no weight, whatever rows are left out."""
+    q, k, v, lens, _ = make(D + T, 1, 2 * G, 2, T, 400, D, [330])
+    q[..., 3] = -1.0 - q[..., 3].abs()
+    lse = torch.from_numpy(OT.tree_attention(q, k, v, lens)[1]).float()
+    row = None
+    if scaled:
+        row = torch.ones(1, T)
+        row[:, ::2] = 0.0
+    at = [0, 5, 130, 255, 300, 329]
+    plain = k.clone()
+    k[:, :, at, 3] = math.inf
+    ref = OT.key_weights(q, plain, lse, lens, None, row)
+    tol = weights_tolerance(q, plain, lse, lens, None, row, None, 1.0, ref)
+    ref[:, :, at], tol[:, :, at] = 0.0, 0.0
+    kw = B.KeyWeights()
+    w = kw(q.cuda(), k.cuda(), lse.cuda(), lens.cuda(), None, None if row is None else row.cuda())
+    assert kw.status() == 0
+    assert (np.abs(w.cpu().double().numpy() - ref) <= tol).all()
+
+
 # ---- eviction ----
 
 def weights_like(g, *shape):
