@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
   uint64_t* p_empty = p_full + 2;      // [PB] P.V done
   uint64_t* drain = p_empty + 2;       // [2]
   uint64_t* voted = drain + 2;         // [groups]
-  int* sOver = reinterpret_cast<int*>(voted + 4);  // [groups][2] tile number + 1 whose scores exceed a maximum by kLazy
+  int* sOver = reinterpret_cast<int*>(voted + 4);  // [groups][2] number + 1 of a tile that moves maxima
   volatile int* s_abort = reinterpret_cast<volatile int*>(sOver + 8);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(s_abort) + 1);
   static_assert(40 + (2 * RING + 16) * 8 + 40 <= 360, "misc");
@@ -551,6 +551,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
                 d = negM[tid] - nm;
                 negM[tid] = nm;
                 sSet[col0 + tid] = 1;
+              } else if (!set) {
+                sOver[2 * grp + (~n & 1)] = n + 2;  // every score -inf so far: the next tile sets the maximum
               }
               alpha[tid] = set ? ex2_approx(-d) : 1.f;  // a row without a maximum has no sums yet
               moved = set && d != 0.f;

@@ -181,6 +181,23 @@ def test_nan_in_a_query_row_stays_in_that_row():
     assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
 
 
+@pytest.mark.parametrize("D,G,T", [(64, 1, 1), (128, 4, 1), (128, 4, 8), (256, 2, 3), (256, 4, 16), (64, 4, 32), (128, 4, 25)])
+def test_leading_keys_that_score_minus_infinity(D, G, T):
+    """A row's first tiles give it no maximum; the later scores are far below 0, so that weights
+    relative to 0 would vanish. Blocks of one tile and of several."""
+    for Bz, Hkv in ((1, 1), (40, 8)):
+        n, skip = 900, 300
+        q, k, v, lens, _ = make(D + T, Bz, G * Hkv, Hkv, T, n + T, D, [n] * Bz)
+        q[..., 3], k[..., 3] = -64.0, 60.0
+        part = k[:, :, skip:].clone(), v[:, :, skip:].clone()
+        k[:, :, :skip, 3] = math.inf
+        out, lse, err = decode(q, k, v, lens)
+        assert err == 0
+        few = slice(0, 3)
+        check_attention(out[few], lse[few], q[few], part[0][few], part[1][few], lens[few] - skip)
+        assert torch.isfinite(lse).all() and torch.isfinite(out).all()
+
+
 def test_empty_trees_and_a_full_cache():
     q, k, v, lens, parents = make(15, 2, 2, 1, 3, 64, 128, [61, 0], [[-2, -2, -2], [-1, -1, -2]])
     out, lse, err = decode(q, k, v, lens, parents)
