@@ -479,8 +479,8 @@ mfa_status mfa_key_weights(const mfa_tensor* q, const mfa_tensor* k, const float
  *            min(n, budget) of them, then -1.
  *   new_lens DEVICE int32 [B]: min(n, budget). Must not be lens.
  * 0 <= recent <= budget, budget >= 1. A length outside [0, N] sets
- * MFA_DEVERR_BOUNDS. Errors: MFA_ERR_INVALID_ARG, MFA_ERR_UNSUPPORTED (N >= 2^30,
- * B * Hkv > 2^24), MFA_ERR_CUDA. */
+ * MFA_DEVERR_BOUNDS. Errors: MFA_ERR_INVALID_ARG, MFA_ERR_UNSUPPORTED (N or budget
+ * >= 2^30, B or Hkv > 65535, B * Hkv > 2^24), MFA_ERR_CUDA. */
 mfa_status mfa_evict_select(const float* weights, const int32_t* lens, int32_t B, int32_t Hkv, int32_t N,
                             int32_t budget, int32_t recent, int32_t* keep, int32_t* new_lens, uint32_t* dev_err,
                             void* stream);
@@ -506,7 +506,8 @@ mfa_status mfa_evict_select(const float* weights, const int32_t* lens, int32_t B
  * that names a row outside [0, N) or fills one outside [0, N_out), moves nothing
  * and sets MFA_DEVERR_SEL. A row may be named more than once. Errors:
  * MFA_ERR_INVALID_ARG (partly overlapping tensors among them),
- * MFA_ERR_SHAPE_MISMATCH, MFA_ERR_UNSUPPORTED, MFA_ERR_CUDA. */
+ * MFA_ERR_SHAPE_MISMATCH, MFA_ERR_UNSUPPORTED (dtype, D, strides; N, N_out or n_idx
+ * >= 2^30; B or Hkv > 65535), MFA_ERR_CUDA. */
 mfa_status mfa_cache_compact(const mfa_tensor* k, const mfa_tensor* v, const float* weights, const int32_t* start,
                              const int32_t* idx, int32_t idx_heads, int32_t n_idx, const int32_t* count,
                              const int32_t* zero_end, const mfa_tensor* k_out, const mfa_tensor* v_out,

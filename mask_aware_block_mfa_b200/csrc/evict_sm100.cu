@@ -237,7 +237,6 @@ constexpr int kMoveThreads = 256;
 struct CompactParams {
   int32_t B, Hkv, idx_heads, n_idx, units;  // units: 16-byte units of a row
   int64_t N, N_out;
-  bool in_place;
   const uint4 *k, *v;
   uint4 *k_out, *v_out;
   int64_t ks[3], vs[3], kos[3], vos[3];  // strides in 16-byte units
@@ -257,12 +256,12 @@ struct Moves {
     count = min(max(p.count[b], 0), p.n_idx);
     idx = p.idx + (static_cast<int64_t>(b) * p.idx_heads + (p.idx_heads == 1 ? 0 : g)) * p.n_idx;
   }
-  // The source row of entry t, or -1 when it moves nothing.
-  __device__ __forceinline__ int64_t source(const CompactParams& p, int t, bool report) const {
+  // The source row of entry t of a move into other tensors, or -1 when it moves nothing.
+  __device__ __forceinline__ int64_t source(const CompactParams& p, int t) const {
     const int64_t x = idx[t];
-    const bool bad = x < 0 || s + x < 0 || s + x >= p.N || s + t < 0 || s + t >= p.N_out || (p.in_place && x < t);
-    if (bad && report) atomicOr(p.err, MFA_DEVERR_SEL);
-    return bad || (p.in_place && x == t) ? -1 : s + x;
+    const bool bad = x < 0 || s + x < 0 || s + x >= p.N || s + t < 0 || s + t >= p.N_out;
+    if (bad) atomicOr(p.err, MFA_DEVERR_SEL);
+    return bad ? -1 : s + x;
   }
 };
 
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(kMoveThreads) mfa_compact_kernel(const __grid_
   if (base >= mv.count) return;
   if (threadIdx.x < kApartRows) {
     const int t = base + threadIdx.x;
-    const int64_t r = t < mv.count ? mv.source(p, t, true) : -1;
+    const int64_t r = t < mv.count ? mv.source(p, t) : -1;
     s_row[threadIdx.x] = r;
     if (w_out && r >= 0) w_out[mv.s + t] = p.w[(static_cast<int64_t>(b) * p.Hkv + g) * p.N + r];
   }
@@ -415,6 +414,11 @@ Range tensor_range(const mfa_tensor* t) {
   return {lo, lo + static_cast<uintptr_t>(last) * 2};
 }
 bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+// Whether the two tensors' first rows share bytes.
+bool share_row(const mfa_tensor* a, const mfa_tensor* b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a->data), y = reinterpret_cast<uintptr_t>(b->data);
+  return (x < y ? y - x : x - y) < static_cast<uintptr_t>(a->D) * 2;
+}
 bool same_tensor(const mfa_tensor* a, const mfa_tensor* b) {
   return a->data == b->data && a->N == b->N && a->stride[0] == b->stride[0] && a->stride[1] == b->stride[1] &&
          a->stride[2] == b->stride[2];
@@ -469,7 +473,7 @@ extern "C" mfa_status mfa_cache_compact(const mfa_tensor* k, const mfa_tensor* v
     if (o->B != k->B || o->H != k->H || o->D != k->D || o->N != k_out->N) return MFA_ERR_SHAPE_MISMATCH;
   if (idx_heads != 1 && idx_heads != k->H) return MFA_ERR_SHAPE_MISMATCH;
   if (k->D % 8 != 0 || k->D > 512) return MFA_ERR_UNSUPPORTED;
-  if (k->B > 65535 || k->H > 65535 || k->N >= (int64_t(1) << 30) || k_out->N >= (int64_t(1) << 30))
+  if (k->B > 65535 || k->H > 65535 || k->N >= (int64_t(1) << 30) || k_out->N >= (int64_t(1) << 30) || n_idx >= (1 << 30))
     return MFA_ERR_UNSUPPORTED;
   if (k->B == 0 || k->N == 0 || k_out->N == 0) return MFA_OK;
   if (!count || (!idx && n_idx > 0)) return MFA_ERR_INVALID_ARG;
@@ -478,9 +482,9 @@ extern "C" mfa_status mfa_cache_compact(const mfa_tensor* k, const mfa_tensor* v
   const Range rk = tensor_range(k), rv = tensor_range(v), ro = tensor_range(k_out), rp = tensor_range(v_out);
   if (in_place) {
     // Interleaved caches (K and V of a token side by side) are in place: they
-    // overlap as ranges but share no row; the same base address does not.
-    if (k->data == v->data) return MFA_ERR_INVALID_ARG;
-  } else if (overlap(rk, ro) || overlap(rk, rp) || overlap(rv, ro) || overlap(rv, rp) || k_out->data == v_out->data) {
+    // overlap as ranges but share no row.
+    if (share_row(k, v)) return MFA_ERR_INVALID_ARG;
+  } else if (overlap(rk, ro) || overlap(rk, rp) || overlap(rv, ro) || overlap(rv, rp) || share_row(k_out, v_out)) {
     return MFA_ERR_INVALID_ARG;
   }
   if (weights) {
@@ -491,7 +495,7 @@ extern "C" mfa_status mfa_cache_compact(const mfa_tensor* k, const mfa_tensor* v
   }
   CompactParams p;
   p.B = static_cast<int32_t>(k->B); p.Hkv = static_cast<int32_t>(k->H); p.idx_heads = idx_heads; p.n_idx = n_idx;
-  p.units = static_cast<int32_t>(k->D / 8); p.N = k->N; p.N_out = k_out->N; p.in_place = in_place;
+  p.units = static_cast<int32_t>(k->D / 8); p.N = k->N; p.N_out = k_out->N;
   p.k = static_cast<const uint4*>(k->data); p.v = static_cast<const uint4*>(v->data);
   p.k_out = static_cast<uint4*>(k_out->data); p.v_out = static_cast<uint4*>(v_out->data);
   for (int a = 0; a < 3; ++a) {

@@ -171,6 +171,13 @@ def test_compact_refuses(lib):
         assert compact_call(lib, k=t[0], v=t[1], ko=t[2], vo=t[3]) == uns
 
 
+def test_compact_refuses_long_lists_and_tensors_whose_rows_share_bytes(lib):
+    assert compact_call(lib, n=1 << 30) == B.MFA_ERR_UNSUPPORTED
+    k, v = tensor((1, 2, 50, 64)), tensor((1, 2, 50, 64), PTR + 64)
+    assert compact_call(lib, k=k, v=v, ko=k, vo=v) == B.MFA_ERR_INVALID_ARG
+    assert compact_call(lib, vo=tensor((1, 2, 20, 64), (1 << 32) + 112)) == B.MFA_ERR_INVALID_ARG
+
+
 def test_null_and_misuse_through_ctypes(lib):
     assert lib.mfa_tree_decode(None, None, None, None, None, None, None, None, 0, None, None) == B.MFA_ERR_INVALID_ARG
     assert lib.mfa_key_weights(None, None, None, None, None, None, None, ctypes.c_float(0), None, None, None) == B.MFA_ERR_INVALID_ARG
