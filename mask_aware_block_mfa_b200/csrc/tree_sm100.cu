@@ -1144,15 +1144,19 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
 // 2^(m_s - M) / sum l_s 2^(m_s - M). A part without a visible key has
 // m = -FLT_MAX, l = 0, o = 0 (never -inf - -inf); all such: out = 0, lse = -inf.
 // A warp takes a row, a lane D / 32 of its columns and, for M and the
-// weights, every 32nd part: two rounds of loads. With few rows (SPLIT) a
-// block takes one row and its warps share the parts.
+// weights, every 32nd part: two rounds of loads. With few rows a block takes one
+// row and its WS warps share the parts: 8 warps while all rows are resident at
+// once (5 blocks per SM), 4 up to 12 rows per SM. (8 lists of 8000 keys, D = 128: 104 rows
+// 18.0 us with 4 against 19.9 with 8 and 23.9 with a warp per row; 4 rows 9.2 with
+// 8, 9.5 with 4; 2048 rows of 128 lists of 4000 49.3 with 4, 47.3 with a warp.)
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
 
-template <int D, int NR, bool SPLIT>
-__global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_constant__ TreeParams p) {
-  constexpr int E = D / 32, WS = SPLIT ? kMergeWarps : 1;
-  __shared__ float so[SPLIT ? kMergeWarps : 1][D];
+template <int D, int NR, int WS>
+__global__ void __launch_bounds__((WS > 1 ? WS : kMergeWarps) * 32) mfa_tree_merge(const __grid_constant__ TreeParams p) {
+  constexpr int E = D / 32;
+  constexpr bool SPLIT = WS > 1;
+  __shared__ float so[WS][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rt = blockIdx.y % p.rtiles;
   const int r = SPLIT ? blockIdx.y / p.rtiles : blockIdx.y / p.rtiles * kMergeWarps + warp;  // row of the row tile
@@ -1211,7 +1215,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mfa_tree_merge(const __grid_
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
-      for (int x = 1; x < kMergeWarps; ++x) o[e] += so[x][lane * E + e];
+      for (int x = 1; x < WS; ++x) o[e] += so[x][lane * E + e];
   }
   const int row = tile.row0 + r, t = p.by_g(row), h = g * p.G + row - t * p.G;
   const bool has = l != 0.f;
@@ -1233,14 +1237,18 @@ struct TreePlan {
   int nr, rtiles, groups, tile_t, parts;
 };
 
+int64_t sm_count() {
+  const int n = device_sm_count();
+  return n > 0 ? n : 148;
+}
+
 // Rows per tile: the smallest of 16, 32, 64, 128 (D = 256: 64) that holds the
 // T nodes' rows, or the largest and several tiles of whole nodes (of parts of one node's
 // heads where G exceeds a tile). CTAs: one per SM, the row tiles side by side
 // on the same keys; with more than 8 row tiles about two per SM instead, so
 // that an uneven number of tiles costs less than the half-empty last wave.
 TreePlan plan_tree(int64_t T, int64_t G, int64_t D) {
-  const int n_sm = device_sm_count();
-  const int64_t sms = n_sm > 0 ? n_sm : 148, R = T * G;
+  const int64_t sms = sm_count(), R = T * G;
   TreePlan pl;
   pl.nr = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 || D == 256 ? 64 : kMaxRows;
   pl.parts = static_cast<int>(cdiv64(G, pl.nr));
@@ -1284,10 +1292,11 @@ mfa_status launch_tree(K kernel, int threads, int bytes, std::atomic<uint64_t>& 
   if (p.groups > 1) {
     const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv;
     const int rows = p.parts > 1 ? NR : p.tile_t * p.G;  // of a tile
-    const bool split = pairs * p.R <= 1024;  // about one wave of blocks (256 and 4096 measured 10 to 20% slower around it)
-    const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>((split ? rows : cdiv64(rows, kMergeWarps)) * p.rtiles));
-    if (!launch_after(split ? mfa_tree_merge<D, NR, true> : mfa_tree_merge<D, NR, false>, grid, kMergeWarps * 32, 0, s, p))
-      return MFA_ERR_CUDA;
+    const int64_t sms = sm_count();
+    const int ws = pairs * p.R <= 5 * sms ? 8 : pairs * p.R <= 12 * sms ? 4 : 1;
+    const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>((ws > 1 ? rows : cdiv64(rows, kMergeWarps)) * p.rtiles));
+    auto* merge = ws == 8 ? mfa_tree_merge<D, NR, 8> : ws == 4 ? mfa_tree_merge<D, NR, 4> : mfa_tree_merge<D, NR, 1>;
+    if (!launch_after(merge, grid, (ws > 1 ? ws : kMergeWarps) * 32, 0, s, p)) return MFA_ERR_CUDA;
   }
   return MFA_OK;
 }

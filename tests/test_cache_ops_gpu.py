@@ -198,6 +198,16 @@ def test_leading_keys_that_score_minus_infinity(D, G, T):
         assert torch.isfinite(lse).all() and torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T", [1, 40, 90])
+def test_pairs_cut_into_many_parts(D, T):
+    """32, 1280 and 2880 rows in all: the merge with eight, four and one warp per row."""
+    q, k, v, lens, parents = make(D + T, 1, 32, 8, T, 1600, D, [1500], "random")
+    out, lse, err = decode(q, k, v, lens, parents)
+    assert err == 0
+    check_attention(out, lse, q, k, v, lens, parents)
+
+
 def test_empty_trees_and_a_full_cache():
     q, k, v, lens, parents = make(15, 2, 2, 1, 3, 64, 128, [61, 0], [[-2, -2, -2], [-1, -1, -2]])
     out, lse, err = decode(q, k, v, lens, parents)
