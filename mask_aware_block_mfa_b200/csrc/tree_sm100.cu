@@ -8,7 +8,7 @@
 // side and share them in L2. Bound: HBM up to about 100 rows (8 x 8 lists of
 // 31,000 keys of 256 columns, 16 rows each: 297 us, 6.9 TB/s), above them the softmax
 // and its exchange with the products (8 x 8 lists of 25,000 keys of 128, 256
-// rows each: 237 us, 715 TFLOP/s; 288 us at the 1.37 GHz of the power limit).
+// rows each: 228 us, 744 TFLOP/s; 276 us where the power limit lowers the clock).
 //
 // Up to 64 rows (and for D = 256) the products are transposed, S^T = K Q^T and
 // O^T += V^T P^T, so that the 128 rows of a tcgen05 MMA are 128 keys (or D
