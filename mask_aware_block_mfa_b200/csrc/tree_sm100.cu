@@ -534,6 +534,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
 #pragma unroll 1
         for (bool again = renew;; again = true) {
           if (renew) {
+            // Warp 3's slot is alpha, which the last tile may still be scaling by: the vote orders that,
+            // the tree's table does, and a chain's tile of drafted keys, which has neither, does here.
+            if (base >= w.len && t > w.t0 && !par) named_barrier(bar, 128);
             scores(x);
 #pragma unroll
             for (int c = 0; c < W; ++c) x[c] = fmaf(x[c], p.scale_log2, negM[c]);

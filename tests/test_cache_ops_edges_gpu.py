@@ -1,0 +1,62 @@
+"""Cache operators on the GPU where tiles, parts and buffers meet: chains over several tiles of
+drafted keys. Against the definition in 64 bits (the tolerances of test_cache_ops_gpu.py)."""
+import math
+
+import pytest
+import torch
+
+from mask_aware_block_mfa_b200 import binding as B
+
+from .cache_util import make, to_gpu
+from .test_cache_ops_gpu import large_tolerance, reference
+
+pytestmark = pytest.mark.gpu
+
+
+def check_large(args, runs):
+    """Equal runs, the first within the tolerance of the definition."""
+    for out, lse in runs[1:]:
+        assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
+    out, lse = runs[0]
+    D = args[0].shape[3]
+    ref_out, ref_lse = reference(args, D)
+    mass, _ = reference(args[:2] + [args[2].abs()] + args[3:], D)
+    tol_out, tol_lse = large_tolerance(args, mass, ref_out, ref_lse)
+    assert ((out.double() - ref_out).abs() <= tol_out).all()
+    assert ((lse.double() - ref_lse).abs() <= tol_lse).all()
+
+
+@pytest.mark.parametrize("D,G,T", [(64, 1, 1), (64, 4, 1), (128, 1, 1), (128, 4, 1), (128, 16, 1), (128, 8, 4), (128, 40, 1), (256, 4, 1),
+                                   (256, 16, 4)])
+def test_a_maximum_that_moves_before_and_in_a_tile_of_drafts_only(D, G, T):
+    """Lengths of whole tiles, so that the drafted keys have a tile of their own, and scores that rise
+    by more than the lazy maximum's slack in the last tile before it and again in it. Blocks of several
+    tiles, with many pairs."""
+    Bz, Hkv, N = 40, 8, 640
+    lens = [128 * (1 + b % 4) for b in range(Bz)]
+    q, k, v, lens, _ = make(D + G, Bz, Hkv * G, Hkv, T, N, D, lens)
+    q[..., 3], k[..., 3] = 8.0, 0.0
+    step = 2.0 * math.sqrt(D)  # 16 in the scores, 23 in powers of two
+    for b in range(Bz):
+        n = int(lens[b])
+        k[b, :, n - 20 + b % 7, 3] = step
+        k[b, :, n + T - 1, 3] = 2 * step
+    args = [to_gpu(x) for x in (q, k, v, lens)] + [None]
+    op = B.TreeDecode()
+    runs = [op(*args) for _ in range(20)]
+    assert op.status() == 0
+    check_large(args, runs)
+
+
+@pytest.mark.parametrize("T,G", [(300, 1), (300, 3), (520, 1)])
+def test_chains_over_several_tiles_of_drafts_in_wide_heads(T, G):
+    """Scores that rise from tile to tile through the drafted keys: every tile moves its rows' maxima."""
+    Bz, Hkv, N, D = 6, 4, 1200, 256
+    q, k, v, lens, _ = make(T + G, Bz, Hkv * G, Hkv, T, N, D, [0, 128, 500, 256, 37, N - T])
+    q[..., 3] = 8.0
+    k[..., 3] = (torch.arange(N) // 64).float() * math.sqrt(D)  # 8 in the scores for every 64 keys
+    args = [to_gpu(x) for x in (q, k, v, lens)] + [None]
+    op = B.TreeDecode()
+    runs = [op(*args) for _ in range(10)]
+    assert op.status() == 0
+    check_large(args, runs)
