@@ -461,7 +461,9 @@ mfa_status mfa_tree_decode(const mfa_tensor* q, const mfa_tensor* k, const mfa_t
  *   row_scale   DEVICE float32 [B, T], or NULL for ones. Rows of scale 0 (the
  *       rejected drafts of a verified tree) are left out whatever they hold.
  *   weights_in  DEVICE float32 [B, Hkv, N] contiguous, or NULL for zeros; may
- *       be weights_out. Not read when decay is 0.
+ *       be weights_out. Not read when decay is 0. A drafted key goes on from
+ *       the entry at its place, which is the caller's to zero before a new key
+ *       takes it (zero_end of mfa_cache_compact does).
  *   weights_out DEVICE float32 [B, Hkv, N] contiguous.
  * Every key's sum is formed by one thread in a fixed order: the result does
  * not change from run to run. T must be at least 1 (T == 0 is
@@ -500,7 +502,8 @@ mfa_status mfa_evict_select(const float* weights, const int32_t* lens, int32_t B
  *            both NULL; in place exactly when k and v are.
  *   zero_end DEVICE int32 [B] or NULL: weights_out[b, g, j] = 0 for
  *            s + count[b] <= j < min(zero_end[b], N_out): the places that the
- *            next keys will take.
+ *            next keys will take. (After an eviction in place zero_end = lens
+ *            clears what moved or left.)
  * Rows not named above are left as they were. In place every entry must
  * satisfy idx[t] >= t (an ascending list does); an entry that does not, or
  * that names a row outside [0, N) or fills one outside [0, N_out), moves nothing

@@ -607,7 +607,8 @@ class KeyWeights(_CacheOp):
         """weights_out[b, g, j] = decay * weights_in[b, g, j] + the rows' softmax weights of key j,
         summed over the group's heads and, times row_scale float32 [B, T], over the rows.
         Weights are float32 [B, Hkv, N]; weights_in None is zeros, and may be weights_out
-        (None: new, zeros past the keys held). q, k, lens, parents, lse: TreeDecode's."""
+        (None: new, zeros past the keys held). A drafted key goes on from what weights_in holds at
+        its place: zeros, for a new key. q, k, lens, parents, lse: TreeDecode's."""
         dev = self.device
         qd, kd = _cache_desc("q", q, dev), _cache_desc("k", k, dev)
         B_, Hq, T, _ = q.shape
@@ -718,7 +719,9 @@ class Evictor(_CacheOp):
 
     def __call__(self, k, v, weights, lens, k_out=None, v_out=None, weights_out=None, zero_end=None, stream=None):
         """Select, then move the kept rows of k, v and weights together, in place or into
-        k_out, v_out and weights_out. Returns keep and new_lens; lens is left to the caller."""
+        k_out, v_out and weights_out. Returns keep and new_lens; lens is left to the caller. In place,
+        zero_end=lens clears the sums that stay behind: where weights go on adding up (KeyWeights with
+        weights_in), the next keys in those places would begin with them."""
         if weights is None:
             raise ValueError("weights must be a float32 [B, Hkv, N] tensor")
         kd, vd, w_p, zero_p, kod, vod, wo_p, B_, H, N = self.compact._tensors(k, v, weights, zero_end, k_out, v_out, weights_out)

@@ -1,6 +1,7 @@
-"""Cache operators on the GPU where tiles, parts and buffers meet: chains over several tiles of
-drafted keys. Against the definition in 64 bits (the tolerances of test_cache_ops_gpu.py)."""
+"""Cache operators on the GPU where tiles, parts and calls meet: chains over several tiles of
+drafted keys, the documented serving step run as a loop. Against the definition in 64 bits (the tolerances of test_cache_ops_gpu.py)."""
 import math
+import os
 
 import pytest
 import torch
@@ -60,3 +61,48 @@ def test_chains_over_several_tiles_of_drafts_in_wide_heads(T, G):
     runs = [op(*args) for _ in range(10)]
     assert op.status() == 0
     check_large(args, runs)
+
+
+def readme_serving_step():
+    """The README's lines from the comment on serving to the end of their block."""
+    with open(os.path.join(os.path.dirname(__file__), "..", "README.md")) as f:
+        block = next(b for b in f.read().split("```") if "# serving from a cache" in b)
+    return block[block.index("# serving from a cache"):]
+
+
+def test_the_readme_step_run_as_a_loop_keeps_no_sums_of_keys_that_left():
+    """Round after round of the documented step: what is behind the keys held has no weight left that
+    the next drafts would begin with, lens follows the eviction, and the sums are those of the keys held."""
+    step = compile(readme_serving_step(), "README.md", "exec")
+    g = torch.Generator(device="cuda").manual_seed(31)
+    Bz, Hkv, G, T, D, N, budget = 2, 2, 2, 6, 64, 8300, 8192
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)
+
+    k, v = rand(Bz, Hkv, N, D), rand(Bz, Hkv, N, D)
+    held = torch.tensor([budget - 3, 100], dtype=torch.int32)
+    names = {"B": B, "k_cache": k, "v_cache": v, "lens": held.cuda(), "T": T, "w": torch.zeros(Bz, Hkv, N, device="cuda"),
+             "parents": torch.tensor([[-1, 0, 0, 1, 2, -1]] * Bz, dtype=torch.int32, device="cuda")}
+    nodes = torch.tensor([[[0, 2, 4]], [[0, 1, 0]]], dtype=torch.int32)
+    count = torch.tensor([3, 2], dtype=torch.int32)
+    rows = torch.zeros(Bz, T)
+    for b in range(Bz):
+        rows[b, nodes[b, 0, :count[b]].long()] = 1.0
+    names |= {"accepted_nodes": nodes.cuda(), "n_accepted": count.cuda(), "accepted": rows.cuda()}
+    for it in range(4):
+        names["q_drafts"] = rand(Bz, Hkv * G, T, D)
+        for b in range(Bz):  # the drafts' keys and values
+            n = int(held[b])
+            k[b, :, n:n + T], v[b, :, n:n + T] = rand(Hkv, T, D), rand(Hkv, T, D)
+        exec(step, names)
+        held = (held + count).clamp_max(budget)
+        for b in range(Bz):
+            assert (names["w"][b, :, int(held[b]):] == 0).all(), it
+        assert torch.equal(names["lens"].cpu(), held), it
+        # An accepted row sees accepted nodes only, so its weights add up to 1 over the keys that stay; an eviction
+        # takes sums away. (Weights are off by the scores' and the lse's error: 2 (D + 4) 2^-23 |q| |k| / sqrt(D),
+        # below 4e-4 for |q|, |k| < 13, and the sums of 8200 keys by 1e-3 / 2.)
+        total = names["w"].double().sum(-1).cpu()
+        want = (it + 1) * G * count.double()[:, None]
+        assert (total <= want * (1 + 1e-3)).all() and (total[1] >= want[1] * (1 - 1e-3)).all()
