@@ -497,7 +497,8 @@ mfa_status mfa_evict_select(const float* weights, const int32_t* lens, int32_t B
  *   k, v     [B, Hkv, N, D]; k_out, v_out [B, Hkv, N_out, D]: bf16, D a multiple
  *            of 8 up to 512, strides and addresses as for mfa_tree_decode.
  *            Either the outputs are the inputs (same addresses and strides: in
- *            place) or they share no byte with them.
+ *            place) or they share no byte with them. No row of k_out shares a
+ *            byte with one of v_out; rows that lie between one another's are fine.
  *   weights [B, Hkv, N], weights_out [B, Hkv, N_out] DEVICE float32 contiguous, or
  *            both NULL; in place exactly when k and v are.
  *   zero_end DEVICE int32 [B] or NULL: weights_out[b, g, j] = 0 for

@@ -1,5 +1,6 @@
 // Eviction from a key/value cache by accumulated attention weight:
 // mfa_evict_select chooses the keys to keep, mfa_cache_compact moves the rows.
+#include <algorithm>
 #include <cuda_bf16.h>
 
 #include "cache.cuh"
@@ -414,10 +415,42 @@ Range tensor_range(const mfa_tensor* t) {
   return {lo, lo + static_cast<uintptr_t>(last) * 2};
 }
 bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-// Whether the two tensors' first rows share bytes.
+// Whether a row of a and a row of b share bytes: a, b [B, H, N, D] of the same sizes with strides s and t,
+// d the elements from a's first row to b's. They do where |d + sum_x (j_x t_x - i_x s_x)| < D for
+// some 0 <= i_x, j_x < n_x. The steps are taken from the largest on, each as often as
+// leaves a rest that the smaller ones can reach: once or twice in layouts that are
+// permutations or slices of a dense one. (Others may take many; those beyond kTries count as sharing.)
+struct Steps {
+  int64_t step, lo, hi;  // taken lo to hi times
+};
+bool reaches(const Steps* at, int n, int64_t d, int64_t D, int* tries) {
+  if (n == 0) return d > -D && d < D;
+  int64_t lo = -D + 1 - d, hi = D - 1 - d;  // what the steps have to come to
+  for (int x = 1; x < n; ++x) {
+    lo -= at[x].hi * at[x].step;
+    hi -= at[x].lo * at[x].step;
+  }
+  const int64_t s = at[0].step;
+  const int64_t first = lo <= 0 ? -(-lo / s) : (lo + s - 1) / s, last = hi >= 0 ? hi / s : -((-hi + s - 1) / s);
+  for (int64_t m = std::max(first, at[0].lo); m <= std::min(last, at[0].hi); ++m)
+    if (--*tries < 0 || reaches(at + 1, n - 1, d + m * s, D, tries)) return true;
+  return false;
+}
 bool share_row(const mfa_tensor* a, const mfa_tensor* b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a->data), y = reinterpret_cast<uintptr_t>(b->data);
-  return (x < y ? y - x : x - y) < static_cast<uintptr_t>(a->D) * 2;
+  constexpr int kTries = 1 << 14;
+  if (!overlap(tensor_range(a), tensor_range(b))) return false;
+  const int64_t count[3] = {a->B, a->H, a->N};
+  Steps at[6];
+  int n = 0, tries = kTries;
+  for (int x = 0; x < 3; ++x) {
+    if (count[x] == 1) continue;
+    const bool same = a->stride[x] == b->stride[x];
+    at[n++] = {b->stride[x], same ? 1 - count[x] : 0, count[x] - 1};
+    if (!same) at[n++] = {a->stride[x], 1 - count[x], 0};
+  }
+  std::sort(at, at + n, [](const Steps& x, const Steps& y) { return x.step > y.step; });
+  const int64_t d = (reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data)) / 2;  // (both on 16 bytes)
+  return reaches(at, n, d, a->D, &tries);
 }
 bool same_tensor(const mfa_tensor* a, const mfa_tensor* b) {
   return a->data == b->data && a->N == b->N && a->stride[0] == b->stride[0] && a->stride[1] == b->stride[1] &&
@@ -481,8 +514,7 @@ extern "C" mfa_status mfa_cache_compact(const mfa_tensor* k, const mfa_tensor* v
   if (in_place != same_tensor(v, v_out)) return MFA_ERR_INVALID_ARG;
   const Range rk = tensor_range(k), rv = tensor_range(v), ro = tensor_range(k_out), rp = tensor_range(v_out);
   if (in_place) {
-    // Interleaved caches (K and V of a token side by side) are in place: they
-    // overlap as ranges but share no row.
+    // (Interleaved caches, K and V of a token side by side, overlap as ranges but share no row.)
     if (share_row(k, v)) return MFA_ERR_INVALID_ARG;
   } else if (overlap(rk, ro) || overlap(rk, rp) || overlap(rv, ro) || overlap(rv, rp) || share_row(k_out, v_out)) {
     return MFA_ERR_INVALID_ARG;

@@ -1,5 +1,5 @@
 """Cache operators on the GPU where tiles, parts and calls meet: chains over several tiles of
-drafted keys, the documented serving step run as a loop. Against the definition in 64 bits (the tolerances of test_cache_ops_gpu.py)."""
+drafted keys, the documented serving step run as a loop, K and V between one another. Against the definition in 64 bits (the tolerances of test_cache_ops_gpu.py)."""
 import math
 import os
 
@@ -106,3 +106,32 @@ def test_the_readme_step_run_as_a_loop_keeps_no_sums_of_keys_that_left():
         total = names["w"].double().sum(-1).cpu()
         want = (it + 1) * G * count.double()[:, None]
         assert (total <= want * (1 + 1e-3)).all() and (total[1] >= want[1] * (1 - 1e-3)).all()
+
+
+LAYOUTS = {  # a buffer's shape from B, H, N, D, and its K and V as [B, H, N, D]
+    "tokens": (lambda b, h, n, d: (b, n, 2, h, d), lambda x: (x[:, :, 0].transpose(1, 2), x[:, :, 1].transpose(1, 2))),
+    "columns": (lambda b, h, n, d: (b, h, n, 2 * d), lambda x: x.chunk(2, -1)),
+    "heads": (lambda b, h, n, d: (b, 2 * h, n, d), lambda x: (x[:, ::2], x[:, 1::2])),
+    "batches": (lambda b, h, n, d: (b, 2, h * n, d),  # K head by head, V token by token
+                lambda x: (x[:, 0].unflatten(1, (3, -1)), x[:, 1].unflatten(1, (-1, 3)).transpose(1, 2))),
+}
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("layout", list(LAYOUTS))
+def test_rows_move_where_k_and_v_lie_between_one_another(layout, in_place):
+    shape, views = LAYOUTS[layout]
+    Bz, H, N, D, n = 2, 3, 500, 64, 200
+    g = torch.Generator(device="cuda").manual_seed(7)
+    buf = torch.randn(shape(Bz, H, N, D), generator=g, device="cuda", dtype=torch.bfloat16)
+    out = buf if in_place else torch.zeros(shape(Bz, H, n, D), dtype=torch.bfloat16, device="cuda")
+    (k, v), (ko, vo) = views(buf), views(out)
+    idx = torch.stack([torch.randperm(N, generator=g, device="cuda")[:n].sort().values for _ in range(Bz * H)]).view(Bz, H, n).int()
+    want_k, want_v = (torch.gather(x, 2, idx.long()[..., None].expand(Bz, H, n, D)) for x in (k, v))
+    rest = [x[:, :, n:].clone() for x in (k, v)]
+    op = B.CacheCompact()
+    op(k, v, idx, torch.full((Bz,), n, dtype=torch.int32, device="cuda"), **({} if in_place else dict(k_out=ko, v_out=vo)))
+    assert op.status() == 0
+    assert torch.equal(ko[:, :, :n], want_k) and torch.equal(vo[:, :, :n], want_v)
+    if in_place:
+        assert torch.equal(k[:, :, n:], rest[0]) and torch.equal(v[:, :, n:], rest[1])
