@@ -662,8 +662,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
           poison = false;
           for (int a = tt; a >= 0; a = tree_up(par, a)) poison |= sBad[a >> 5] >> (a & 31) & 1u;
         }
-        // -1: no output.
-        delta[tid] = sum == 0.f ? -1.f : (poison ? NAN : (whole ? 1.f / sum : 1.f));
+        // -1: no output. (A part without weights still makes a row that sees such a node NaN, as
+        // the pair's sum does where it is not cut.)
+        delta[tid] = sum == 0.f && (whole || dead || !poison) ? -1.f : (poison ? NAN : (whole ? 1.f / sum : 1.f));
         if (whole) {
           p.lse[(static_cast<int64_t>(w.b) * p.Hq + h) * p.T + tt] =
               sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
@@ -1089,6 +1090,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
         }
         const float g = poison ? NAN : whole ? 1.f / sum : 1.f;
         const float g0 = f0 * g, g1 = f1 * g;
+        const float none = poison && !whole && !dead ? NAN : 0.f;  // (as in mfa_tree_kernel)
         const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * NR + r;
         const int h = w.g * p.G + head;
         if (real && grp == 0) {
@@ -1111,7 +1113,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, 1)
           for (int u = 0; u < 16; ++u) {
             y[u] = has0 ? __uint_as_float(o0[u]) * g0 : 0.f;
             if (has1) y[u] = fmaf(__uint_as_float(o1[u]), g1, y[u]);
-            if (!any) y[u] = 0.f;
+            if (!any) y[u] = none;
           }
           if (real) {
             if (whole) {

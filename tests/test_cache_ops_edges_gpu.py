@@ -135,3 +135,32 @@ def test_rows_move_where_k_and_v_lie_between_one_another(layout, in_place):
     assert torch.equal(ko[:, :, :n], want_k) and torch.equal(vo[:, :, :n], want_v)
     if in_place:
         assert torch.equal(k[:, :, n:], rest[0]) and torch.equal(v[:, :, n:], rest[1])
+
+
+@pytest.mark.parametrize("D,G,T,tree", [(64, 2, 1, False), (128, 4, 1, False), (256, 2, 3, False), (128, 2, 6, True), (64, 2, 40, False),
+                                        (128, 4, 30, True)])
+def test_a_broken_value_reaches_its_rows_whatever_the_key_scores(D, G, T, tree):
+    """Node 0's value holds an infinity and its key scores -inf: rows that see it are NaN in all columns, whether
+    a pair is cut in front of the drafted keys' tile (few pairs) or not (many). A padding node changes nothing."""
+    for Bz, Hkv in ((1, 1), (40, 8)):
+        n = 256
+        parents = None
+        if tree:  # every second node follows node 0, the others the sequence; the last place is empty
+            parents = [[-2 if t == T - 1 else (0 if t % 2 == 0 and t > 0 else -1) for t in range(T)]] * Bz
+        q, k, v, lens, parents = make(D + T, Bz, G * Hkv, Hkv, T, n + T, D, [n] * Bz, parents)
+        q[..., 3] = -1.0 - q[..., 3].abs()
+        clean = [to_gpu(x) for x in (q, k, v, lens, parents)]
+        k[:, :, n, 3], v[:, :, n, 5] = math.inf, math.inf
+        if tree:
+            v[:, :, n + T - 1] = math.inf
+        op = B.TreeDecode()
+        ref, _ = op(*clean)
+        out, lse = op(*[to_gpu(x) for x in (q, k, v, lens, parents)])
+        assert op.status() == 0
+        for t in range(T):
+            if tree and t == T - 1:
+                assert (out[:, :, t] == 0).all() and torch.isneginf(lse[:, :, t]).all()
+            elif tree and t % 2 == 1:
+                assert torch.equal(out[:, :, t], ref[:, :, t])
+            else:
+                assert torch.isnan(out[:, :, t]).all() and torch.isfinite(lse[:, :, t]).all(), t
