@@ -25,15 +25,6 @@ __device__ __forceinline__ int tree_up(const T* par, int t) {
   return (p < 0 || p >= t) ? -1 : (par[p] == -2 ? -1 : p);
 }
 
-// Whether row t sees node n's key (n == t: its own). parents NULL: a chain.
-__device__ __forceinline__ bool tree_sees(const int32_t* par, int t, int n) {
-  if (par == nullptr) return n <= t;
-  if (n > t || par[t] == -2) return false;
-  int a = t;
-  while (a > n) a = tree_up(par, a);
-  return a == n;
-}
-
 // Division of numbers below 2^31 by a divisor known on the host: with
 // 2^(shift - 1) < d <= 2^shift and mul = ceil(2^(31 + shift) / d), n mul / 2^(31 + shift)
 // exceeds n / d by less than n / 2^31 / d < 1 / d.

@@ -98,7 +98,7 @@ __device__ __forceinline__ void load_q(const TreeParams& p, const CUtensorMap* t
 // ---------------------------------------------------------------------------
 template <int D, int NR>
 struct Cfg {
-  static constexpr int kCols = 16;                      // rows (registers) per softmax thread
+  static constexpr int kCols = 16;                      // rows (registers) per softmax thread, as wide as the loads from TMEM
   static constexpr int kGroups = NR / kCols;            // groups of 4 softmax warps
   static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kThreads = (kSoftWarps + 4) * 32;  // + S, P.V, TMA of K and V, TMA of Q
@@ -129,46 +129,20 @@ __device__ __forceinline__ float warp_max(float x) {  // NaN is ignored unless a
   return y;
 }
 
-template <int C>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float (&x)[C]) {
-  if constexpr (C == 16) {
-    uint32_t r[16];
-    tmem_ld_32x32b_x16(addr, r);
-    tmem_ld_wait();
+// Reduces v[c] over the warp's lanes: lane l ends with the result of column l / 2 in
+// v[0], by halvings that hand half of the columns on.
+template <typename Op>
+__device__ __forceinline__ float warp_reduce_spread(float (&v)[16], int lane, Op op) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(r[c]);
-  } else {
-    uint32_t r[C / 32][32];
+  for (int w = 16, n = 8; w > 1; w >>= 1, n >>= 1) {
+    const bool up = lane & w;
 #pragma unroll
-    for (int k = 0; k < C / 32; ++k) tmem_ld_32x32b_x32(addr + k * 32, r[k]);
-    tmem_ld_wait();
-#pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = __uint_as_float(r[c >> 5][c & 31]);
-  }
-}
-
-// Reduces v[c] over the warp's lanes: lane l ends with the result of column l
-// (C = 16: l / 2) in v[0], by halvings that hand half of the columns on.
-template <int C, typename Op>
-__device__ __forceinline__ float warp_reduce_spread(float (&v)[C], int lane, Op op) {
-  int n = C;
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
-    if (n > 1) {
-      n >>= 1;
-      const bool up = lane & w;
-#pragma unroll
-      for (int c = 0; c < C / 2; ++c) {
-        if (c < n) {
-          const float give = up ? v[c] : v[c + n], keep = up ? v[c + n] : v[c];
-          v[c] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
-        }
-      }
-    } else {
-      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], w));
+    for (int c = 0; c < n; ++c) {
+      const float give = up ? v[c] : v[c + n], keep = up ? v[c + n] : v[c];
+      v[c] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
     }
   }
-  return v[0];
+  return v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 // By the warp that issues P.V, before tile t's: V of a key that is not before
@@ -516,7 +490,11 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
           }
         }
         auto scores = [&](float (&y)[W]) {
-          tmem_ld_cols<W>(st, y);
+          uint32_t r[W];
+          tmem_ld_32x32b_x16(st, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < W; ++c) y[c] = __uint_as_float(r[c]);
           if (draft) {
 #pragma unroll
             for (int c = 0; c < W; ++c)
@@ -540,9 +518,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
             scores(x);
 #pragma unroll
             for (int c = 0; c < W; ++c) x[c] = fmaf(x[c], p.scale_log2, negM[c]);
-            float m = warp_reduce_spread<W>(x, lane, [](float a, float b) { return fmaxf(a, b); });
-            if (quad > 0) slot[lane / (32 / W)] = m;  // (W = 16: two lanes write the same value)
-            if (W == 16) m = __shfl_sync(0xffffffffu, m, (lane & 15) * 2);
+            float m = warp_reduce_spread(x, lane, [](float a, float b) { return fmaxf(a, b); });
+            if (quad > 0) slot[lane / 2] = m;  // (two lanes write the same value)
+            m = __shfl_sync(0xffffffffu, m, (lane & 15) * 2);
             named_barrier(bar, 128);
             bool moved = false;
             if (tid < W) {
@@ -571,14 +549,13 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
               mbar_wait(&p_empty[(n - 1) % PB], ((n - 1) / PB) & 1, s_abort);
               tc_fence_after();
 #pragma unroll 1
-              for (int k = 0; k < U * (W / 16); ++k) {
-                const int c = (k % (W / 16)) * 16;
-                const uint32_t at = tm + C::kO + (k / (W / 16)) * NR + c;
+              for (int u = 0; u < U; ++u) {
+                const uint32_t at = tm + C::kO + u * NR;
                 uint32_t o[16];
                 tmem_ld_32x32b_x16(at, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[c + i]);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[i]);
                 tmem_st_32x32b_x16(at, o);
               }
               tmem_st_wait();
@@ -645,9 +622,9 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
         float v[W];
 #pragma unroll
         for (int c = 0; c < W / 2; ++c) f2_unpack(l[c], v[2 * c], v[2 * c + 1]);
-        part_sum = warp_reduce_spread<W>(v, lane, [](float a, float b) { return a + b; });
-        if (quad > 0) slot[lane / (32 / W)] = part_sum;
-        if (W == 16) part_sum = __shfl_sync(0xffffffffu, part_sum, (lane & 15) * 2);
+        part_sum = warp_reduce_spread(v, lane, [](float a, float b) { return a + b; });
+        if (quad > 0) slot[lane / 2] = part_sum;
+        part_sum = __shfl_sync(0xffffffffu, part_sum, (lane & 15) * 2);
       }
       named_barrier(bar, 128);
       if (tid < rows && tid < W) {
@@ -678,29 +655,28 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1)
       }
       named_barrier(bar, 128);
 #pragma unroll 1
-      for (int k = 0; k < U * (W / 16); ++k) {
-        const int u = k / (W / 16), c0 = (k % (W / 16)) * 16;
+      for (int u = 0; u < U; ++u) {
         const int d = u * 128 + tid;
-        if (c0 >= rows) continue;
+        if (rows <= 0) break;
         uint32_t o[16];
-        tmem_ld_32x32b_x16(tm + C::kO + u * NR + c0, o);
+        tmem_ld_32x32b_x16(tm + C::kO + u * NR, o);
         tmem_ld_wait();
         if (d < D) {
           if (whole) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              if (c0 + i >= rows) break;
-              const float f = delta[c0 + i];
-              const int64_t to = static_cast<int64_t>(static_cast<uint32_t>(reinterpret_cast<const int*>(negM)[c0 + i])) |
-                                 (static_cast<int64_t>(reinterpret_cast<const int*>(alpha)[c0 + i]) << 32);
+              if (i >= rows) break;
+              const float f = delta[i];
+              const int64_t to = static_cast<int64_t>(static_cast<uint32_t>(reinterpret_cast<const int*>(negM)[i])) |
+                                 (static_cast<int64_t>(reinterpret_cast<const int*>(alpha)[i]) << 32);
               p.out[to + d] = __float2bfloat16_rn(f == -1.f ? 0.f : __uint_as_float(o[i]) * f);
             }
           } else {
-            float* to = p.o_part + (part + c0) * D + d;
+            float* to = p.o_part + part * D + d;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              if (c0 + i >= rows) break;
-              const float f = delta[c0 + i];
+              if (i >= rows) break;
+              const float f = delta[i];
               to[i * D] = f == -1.f ? 0.f : __uint_as_float(o[i]) * f;
             }
           }
