@@ -5,8 +5,8 @@
 // S^T = K Q^T on tcgen05 as in tree decode, 128 keys by the R = T * G rows of a
 // key/value head, so that a thread holds one key's scores for 16 to 128 rows at
 // a time and adds its own key's weight: no sum crosses threads but the one
-// over row tiles. K is read once for up to 256 rows, and nothing else of size
-// is. Bound: HBM (2 D bytes per key) up to about 150 rows, beyond them the
+// over row tiles. K is read once for up to 256 rows (128 at D = 256), and nothing
+// else of size is. Bound: HBM (2 D bytes per key) up to about 150 rows, beyond them the
 // 16 exponentials per clock of an SM. (4 x 8 lists of 32768 keys, 128 rows: 50
 // us, 5.4 TB/s, 64 us at the 1.5 GHz of the power limit; 8 x 8 lists of 22,000, 64 rows: 61 us, 6.1 TB/s.)
 //
@@ -56,6 +56,12 @@ struct Cfg {
   static constexpr int rest(int qtiles, int T, int words) {
     return kChunk + qtiles * NR * 4 + 2 * kSoftThreads * 4 + 32 + (words > 0 ? T * 4 + T * words * 4 : 0) + 16 + kBars * 8 + 16;
   }
+  // K units beside them.
+  static constexpr int units(int qtiles, int T, int words) { return (kSmem - qtiles * kQTile - rest(qtiles, T, words)) / kUnit; }
+  // Two row tiles in one pass: up to 64 rows are one tile, and at D = 256 two of 128 (64 KB each) leave no ring
+  // of two K tiles. More than two would not help: with two the exponentials already take longer than K's next read.
+  static constexpr bool kTwo = NR == 128 && D < 256;
+  static_assert(units(kTwo ? 2 : 1, MFA_TREE_MAX_NODES, MFA_TREE_MAX_NODES / 32) >= 2 * kUnits, "ring");
 };
 
 template <int D, int NR>
@@ -65,11 +71,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int U = C::kUnits, X = NR < 32 ? NR : 32;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qtiles = C::kTwo ? p.qtiles : 1;
   uint8_t* sQ = smem + p.ring * C::kUnit;                              // [qtiles]
   // 128-byte rows: the rows' constants, 32 bytes for each row tile, and from byte 96 on the keys' ones, 1 1 1 0 ..
-  uint8_t* sConst = sQ + p.qtiles * C::kQTile;                         // [128]
+  uint8_t* sConst = sQ + qtiles * C::kQTile;                           // [128]
   float* sSign = reinterpret_cast<float*>(sConst + kChunk);            // [qtiles * NR] of the row's scale; 0: it is left out
-  float* sPart = sSign + p.qtiles * NR;                                // [2][kGroups][128]
+  float* sPart = sSign + qtiles * NR;                                  // [2][kGroups][128]
   uint32_t* sActive = reinterpret_cast<uint32_t*>(sPart + 2 * kSoftThreads);  // [8] bits: the row counts
   uint64_t* full = reinterpret_cast<uint64_t*>(sActive + 8);           // [ring]
   uint64_t* empty = full + kMaxRing;
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     do {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(q_full, seg & 1, s_abort));
       for (int t = w.t0; t < w.t1 && ok; ++t) {
-        for (int rt = 0; rt < p.qtiles; ++rt, ++item) {
+        for (int rt = 0; rt < qtiles; ++rt, ++item) {
           // The K units, and the buffer as its last sums were read (at once for the first uses: their phase is before the first).
           const int buf = item % C::kBufs;
           const uint32_t free = (item / C::kBufs + 1) & 1;
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A failed wait raises *s_abort and the thread runs on (every later wait
     // then fails at once): the barriers below need all threads.
     const int grp = warp >> 2, tid = threadIdx.x & 127;
-    const int rt = grp & (p.qtiles - 1), nn = kGroups / p.qtiles;  // the group's row tile; tiles in flight
+    const int rt = grp & (qtiles - 1), nn = kGroups / qtiles;  // the group's row tile; tiles in flight
     const uint32_t tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     for (int i = threadIdx.x; i < kKeys * 2; i += kSoftThreads) {
       const int r = i >> 1, u = i & 1;
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // no exponential survives.
       {
         const int i = threadIdx.x, r = i % NR, q = i / NR;
-        const bool real = i < p.qtiles * NR;
+        const bool real = i < qtiles * NR;
         float c = -1e30f;
         sign = 0.f;
         if (real && p.row0 + i < p.R && pre.scale != 0.f && pre.lse != -INFINITY && pre.up != -2) {
@@ -284,12 +291,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int a = sPar[t] == -2 ? -1 : t; a >= 0; a = tree_up(sPar, a)) sSeen[t * p.words + (a >> 5)] |= 1u << (a & 31);
         }
       }
-      for (int i0 = qr; i0 < p.qtiles * NR; i0 += kBatch * kStep) {
+      for (int i0 = qr; i0 < qtiles * NR; i0 += kBatch * kStep) {
         if (i0 != qr) fetch_q(i0);
 #pragma unroll
         for (int y = 0; y < kBatch; ++y) {
           const int i = i0 + y * kStep, r = i % NR;
-          if (i >= p.qtiles * NR) break;
+          if (i >= qtiles * NR) break;
           if (sSign[i] == 0.f) pre.q[y] = make_uint4(0u, 0u, 0u, 0u);
           *reinterpret_cast<uint4*>(sQ + (i / NR) * C::kQTile + (qu >> 3) * (NR * 128) + r * 128 + (((qu & 7) ^ (r & 7)) << 4)) = pre.q[y];
         }
@@ -301,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t out0 = (static_cast<int64_t>(w.b) * p.Hkv + w.g) * p.N;
       const int end = min(w.len + p.T, p.N);
       for (int t = w.t0; t < w.t1; ++t, ++n) {
-        if (n % nn != grp / p.qtiles) continue;
+        if (n % nn != grp / qtiles) continue;
         const int j = t * kKeys + tid, node = j - w.len;
         const bool mine = rt == 0 && j < end, add = p.w_in != nullptr && p.decay != 0.f;
         float old = 0.f;
@@ -313,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&s_full[buf], (k / kEach) & 1, s_abort);
         tc_fence_after();
         // S of the tile's last row tile is done, and so those before it: K may be overwritten.
-        if (rt == p.qtiles - 1 && tid < U) mbar_arrive(&empty[(n * U + tid) % p.ring]);
+        if (rt == qtiles - 1 && tid < U) mbar_arrive(&empty[(n * U + tid) % p.ring]);
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
         bool plain = t * kKeys + kKeys <= w.len && !minus;
         if (plain) {
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float lo, hi;
         f2_unpack(both, lo, hi);
         float sum = lo + hi;
-        if (p.qtiles > 1) {
+        if (qtiles > 1) {
           // The row tiles' sums, in their order. (The barrier of the next tile is
           // passed only once these have been read: two buffers suffice.)
           float* part = sPart + (k & 1) * kSoftThreads;
@@ -405,13 +412,8 @@ mfa_status launch_weights(const CUtensorMap& mk, KeyWeightParams p, cudaStream_t
   const int sms = device_sm_count();
   p.ctas = sms > 0 ? sms : 148;
   for (p.row0 = 0; p.row0 < p.R; p.row0 += p.qtiles * NR) {
-    // Two row tiles in one pass where shared memory holds them beside a ring of two tiles: more
-    // would not help, as with two the exponentials already take longer than K's next read.
-    const int left = static_cast<int>(cdiv64(p.R - p.row0, NR));
-    p.qtiles = left >= 2 ? 2 : 1;
-    auto units = [&](int q) { return (kSmem - q * C::kQTile - C::rest(q, p.T, p.words)) / C::kUnit; };
-    if (units(p.qtiles) < 2 * C::kUnits) p.qtiles = 1;
-    p.ring = units(p.qtiles);
+    p.qtiles = C::kTwo && p.R - p.row0 > NR ? 2 : 1;
+    p.ring = C::units(p.qtiles, p.T, p.words);
     if (p.ring > kMaxRing) p.ring = kMaxRing;
     const int bytes = p.ring * C::kUnit + p.qtiles * C::kQTile + C::rest(p.qtiles, p.T, p.words);
     if (!launch_after(mfa_key_weights_kernel<D, NR>, dim3(p.ctas), kThreads, bytes, s, mk, p)) return MFA_ERR_CUDA;
