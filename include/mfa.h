@@ -432,7 +432,10 @@ mfa_status mfa_decode(const mfa_tensor* q, const mfa_tensor* k, const mfa_tensor
 size_t mfa_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t D);
 
 /* Attention of T drafted tokens per sequence over the cache, on `stream`:
- * out = softmax(q k^T / sqrt(D)) v over the keys each row sees.
+ * out = softmax(q k^T / sqrt(D)) v over the keys each row sees. Scores, maxima
+ * and sums are float32; as in mfa_fwd and mfa_decode the weights enter the product
+ * with v as bf16 (off by at most 2^-8 of each; the sum that divides it is of the
+ * unrounded ones).
  *   q, out  [B, Hq, T, D] bf16;  k, v [B, Hkv, N, D] bf16;  D in {64, 128, 256};
  *           Hq % Hkv == 0 (any group size); stride[3] == 1, other strides
  *           and base addresses 16-byte aligned. 1 <= N < 2^30.

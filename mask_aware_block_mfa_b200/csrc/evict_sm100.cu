@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(kMoveThreads) mfa_compact_kernel(const __grid_
 // one writes, so they are loaded before, and the list one chunk earlier still. Blocks share
 // nothing: each moves its own slice of the columns of one head's K or V, one more block the weights.
 // Entries per thread and chunk (BATCH): 8 for long lists (64 lists of 8192 of 32768 rows of
-// 128: 102 us, 5.3 TB/s; with 4, or slices of 8 or 16 units, 104 to 157 us), 2 where
-// that takes the whole list in a chunk (6 rows of 64 heads: 3.5 us against 9.1, as more blocks fit an SM).
+// 128: 101 us, 5.4 TB/s; with 4, or slices of 8 or 16 units, 104 to 157 us), 2 where
+// that takes the whole list in a chunk (6 rows of 64 heads: 3.8 us against 9.9, as more blocks fit an SM).
 constexpr int kSlice = 4;   // 16-byte units of a row per block
 constexpr int kShort = 2 * (kMoveThreads / kSlice);
 

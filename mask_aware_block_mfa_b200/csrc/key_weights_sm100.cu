@@ -7,8 +7,8 @@
 // a time and adds its own key's weight: no sum crosses threads but the one
 // over row tiles. K is read once for up to 256 rows (128 at D = 256), and nothing
 // else of size is. Bound: HBM (2 D bytes per key) up to about 150 rows, beyond them the
-// 16 exponentials per clock of an SM. (4 x 8 lists of 32768 keys, 128 rows: 50
-// us, 5.4 TB/s, 64 us at the 1.5 GHz of the power limit; 8 x 8 lists of 22,000, 64 rows: 61 us, 6.1 TB/s.)
+// 16 exponentials per clock of an SM. (4 x 8 lists of 32768 keys, 128 rows: 52
+// us, 5.3 TB/s, 64 us at the 1.5 GHz of the power limit; 8 x 8 lists of 22,000, 64 rows: 62 us, 6.0 TB/s.)
 //
 // What a row adds to every score, -lse and the logarithm of its scale's size, would cost
 // each thread a shared-memory read per row (as much of the SM's time as the

@@ -6,9 +6,9 @@
 // (row t * G + h') read the same keys, so K and V are read once for a tile of
 // up to 128 rows; with more rows the CTAs of the row tiles walk the same keys side by
 // side and share them in L2. Bound: HBM up to about 100 rows (8 x 8 lists of
-// 31,000 keys of 256 columns, 16 rows each: 297 us, 6.9 TB/s), above them the softmax
+// 31,000 keys of 256 columns, 16 rows each: 295 us, 7.0 TB/s), above them the softmax
 // and its exchange with the products (8 x 8 lists of 25,000 keys of 128, 256
-// rows each: 228 us, 744 TFLOP/s; 276 us where the power limit lowers the clock).
+// rows each: 238 us, 713 TFLOP/s; 288 us where the power limit lowers the clock).
 //
 // Up to 64 rows (and for D = 256) the products are transposed, S^T = K Q^T and
 // O^T += V^T P^T, so that the 128 rows of a tcgen05 MMA are 128 keys (or D
@@ -1226,8 +1226,9 @@ int64_t sm_count() {
 // Rows per tile: the smallest of 16, 32, 64, 128 (D = 256: 64) that holds the
 // T nodes' rows, or the largest and several tiles of whole nodes (of parts of one node's
 // heads where G exceeds a tile). CTAs: one per SM, the row tiles side by side
-// on the same keys; with more than 8 row tiles about two per SM instead, so
-// that an uneven number of tiles costs less than the half-empty last wave.
+// on the same keys. With more than 8 row tiles that could leave a quarter of the SMs idle
+// (38 x 3 of 148), so that each gets its part of two CTAs per SM, rounded up: 9 x 33,
+// 16 x 19 or 32 x 10 on 148 SMs, of which the few past 296 run in a third wave.
 TreePlan plan_tree(int64_t T, int64_t G, int64_t D) {
   const int64_t sms = sm_count(), R = T * G;
   TreePlan pl;
